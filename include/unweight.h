@@ -399,6 +399,113 @@ int uw_mlp_layer(const uw_dmat* gate, const uw_dmat* up, const uw_dmat* down, in
                  const uint16_t* X, int64_t batch, float* y,
                  void* scratch, uint64_t scratch_bytes, void* stream, void* aux_stream);
 
+/* ---------------------------------- matmul with an epilogue, mixture of experts */
+/* Operators of an LLM's serving path around the matmuls above; the pages
+ * define none of them (API).  A weight is given as `w` (bf16 bits, device)
+ * or as `d` (a compressed matrix with its NIB section, as
+ * uw_gemm_recon_pal's), the other NULL.  The matrices of a layer's experts
+ * are ONE matrix [experts*rows, cols], expert e its rows e*rows ..: one
+ * uw_compress, one descriptor, one palette.  One expert's matrix holds fewer
+ * than 2^31 weights; all of them together may hold more.
+ * Activations are bf16 with a row stride ld (elements, a multiple of 8 for
+ * the X of a matmul); sums are fp32 and rounded once, to the output's type.
+ * Outputs may have any row stride of at least their width; elements between
+ * the rows are left as they were.  UW_EINVAL: a shape, stride, type, NULL or
+ * misaligned pointer (16 bytes), a scratch too small, an output that overlaps
+ * an input it must not; UW_EUNSUPPORTED: 2^31 weights or more in a matrix.
+ * Nothing is allocated, no call waits for the device, and every call may be
+ * captured into a graph. */
+enum { UW_F32 = 0, UW_BF16 = 1 };                  /* value types */
+enum {                                             /* activations, in fp32 */
+    UW_ACT_NONE = 0,
+    UW_ACT_RELU = 1,
+    UW_ACT_SILU = 2,       /* v / (1 + exp(-v)) */
+    UW_ACT_GELU = 3,       /* v/2 (1 + erf(v / sqrt 2)) */
+    UW_ACT_GELU_TANH = 4   /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+};
+
+/* out[b][r] = act(sum_c X[b][c] W[r][c] + bias[r]) + residual[b][r].
+ * bias [rows] and residual [batch, rows] may be NULL; out may be the residual
+ * itself (same pointer, stride and type), and overlaps nothing else.
+ * scratch: NULL, or uw_linear_scratch_bytes() bytes for the sums of K-slices
+ * that fill the chip when batch and rows are small (without it K is not
+ * split over workgroups); calls that share it must be ordered. */
+int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols,
+              const uint16_t* X, int64_t ldx, int64_t batch,
+              const void* bias, int bias_type, int act,
+              const void* residual, int residual_type, int64_t ldr,
+              void* out, int out_type, int64_t ldo,
+              void* scratch, uint64_t scratch_bytes, void* stream);
+
+/* Scratch of uw_linear on the current device (>= 0, 0: none) or an error code. */
+int64_t uw_linear_scratch_bytes(int64_t rows, int64_t cols, int64_t batch);
+
+/* The router's selection.  Of each token's `experts` logits (fp32 or bf16, row
+ * stride ld) the top_k largest are chosen, equal ones by the lowest index:
+ *   ids[t][j]     the j-th largest's expert
+ *   weights[t][j] exp(l_j - max) / sum exp(l_i - max), the sum over the chosen
+ *                 experts (renormalize != 0) or over all
+ * and the slots t*top_k + j are grouped by expert, in ascending order inside
+ * each, so results do not vary from call to call:
+ *   offsets[e]    the first row of expert e, [experts] the number of rows
+ *   order[s]      the slot of row s
+ *   place[t][j]   the row of slot t*top_k + j
+ * -inf and NaN logits are never chosen and count for nothing, +inf is the
+ * largest finite number.  A token with fewer than top_k others (a padded one
+ * has none) gets id -1, weight 0 and place -1 in its last slots; order is -1
+ * behind the last row.  experts <= 512, top_k <= 16, tokens * top_k < 2^31.
+ * scratch: uw_moe_route_scratch_bytes() bytes (0 through 64 tokens). */
+int uw_moe_route(const void* logits, int logits_type, int64_t ld, int64_t tokens, int experts,
+                 int top_k, int renormalize, int32_t* ids, float* weights, int32_t* offsets,
+                 int32_t* order, int32_t* place, void* scratch, uint64_t scratch_bytes,
+                 void* stream);
+int64_t uw_moe_route_scratch_bytes(int64_t tokens, int experts, int top_k);
+
+/* Matmul grouped by expert: out[s] = W_e . X[x(s)] for the rows s in
+ * offsets[e] .. offsets[e+1]-1 of every expert e, x(s) = s, or
+ * order[s] / top_k where order is given (the slots of uw_moe_route).
+ * offsets (int32 [experts+1]) and order (int32 [n]) are read on the device; n
+ * bounds the rows (out has n), x_rows those of X.  Rows of out outside every
+ * expert's are left as they were.  Offsets that do not ascend within 0..n
+ * are clamped and an index outside X reads row 0: no access leaves the
+ * arrays.  Experts without rows cost nothing. */
+int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t rows, int64_t cols,
+                    const uint16_t* X, int64_t x_rows, int64_t ldx,
+                    const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
+                    void* out, int out_type, int64_t ldo, void* stream);
+
+/* The gate/up pair grouped by expert, h[s] = bf16(SiLU(G_e . x) * (U_e . x)),
+ * rows and inputs as uw_gemm_grouped's; gate and up both bf16 or both
+ * compressed. */
+int uw_moe_gate_up(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* up_w, const uw_dmat* up_d,
+                   int experts, int64_t rows, int64_t cols,
+                   const uint16_t* X, int64_t x_rows, int64_t ldx,
+                   const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
+                   uint16_t* h, int64_t ldh, void* stream);
+
+/* out[t] = sum_j weights[t][j] * Y[place[t][j]] + residual[t] over the j with
+ * 0 <= place < n, in ascending j; Y fp32 [n, cols], residual may be NULL and
+ * may be out. */
+int uw_moe_combine(const float* Y, int64_t n, int64_t cols, const int32_t* place, const float* weights,
+                   int64_t tokens, int top_k, const void* residual, int residual_type, int64_t ldr,
+                   void* out, int out_type, int64_t ldo, void* stream);
+
+/* A whole layer: uw_moe_route on the logits, gate/up, down on the bf16 h, and
+ * the weighted sum, out[t] = sum_j w_j down_e(h_tj) + residual[t].  gate and up
+ * [experts*rows, cols], down [experts*cols, rows], rows and cols multiples of
+ * 64; residual may be NULL; out may be X or the residual (same stride and
+ * type as the residual).  scratch: uw_moe_scratch_bytes() bytes; calls that
+ * share it must be ordered. */
+int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* up_w, const uw_dmat* up_d,
+                 const uint16_t* down_w, const uw_dmat* down_d,
+                 int experts, int64_t rows, int64_t cols,
+                 const uint16_t* X, int64_t ldx, int64_t tokens,
+                 const void* logits, int logits_type, int64_t ldl, int top_k, int renormalize,
+                 const void* residual, int residual_type, int64_t ldr,
+                 void* out, int out_type, int64_t ldo,
+                 void* scratch, uint64_t scratch_bytes, void* stream);
+int64_t uw_moe_scratch_bytes(int64_t tokens, int experts, int top_k, int64_t rows, int64_t cols);
+
 /* ----------------------------------------------------------- kernel timer */
 /* (API) Per-launch durations of the matmul kernels (GEMV and MFMA), for measuring
  * them on their own stream.  While enabled, each matmul kernel launch takes

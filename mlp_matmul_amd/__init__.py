@@ -12,11 +12,13 @@ matmul ("How the reconstructive matmul works").
 from __future__ import annotations
 
 import ctypes as ct
+from typing import NamedTuple
 
 import numpy as np
 
 from ._capi import (  # noqa: F401
     SECTION_NAMES, UW_KERNEL_AUTO, UW_KERNEL_GEMV, UW_KERNEL_MFMA, UW_KERNEL_SKINNY, UW_NUM_SECTIONS,
+    UW_ACT_GELU, UW_ACT_GELU_TANH, UW_ACT_NONE, UW_ACT_RELU, UW_ACT_SILU, UW_BF16, UW_F32,
     UW_PIPE_AUTO, UW_PIPE_BF16, UW_PIPE_DIRECT, UW_PIPE_EXP, UW_PIPE_FULL, UW_PIPE_HUFF, UW_PIPE_PAL,
     UW_SEC_BITMAP, UW_SEC_DLUT, UW_SEC_GLEN, UW_SEC_MLUT, UW_SEC_NIB, UW_SEC_SM, UW_SEC_STREAM,
     UW_SEC_TILE_OFF, UW_SEC_TILE_VBASE, UW_SEC_VEXP, UW_EUNSUPPORTED, UW_EINVAL, UW_STATIC_SCRATCH_BYTES,
@@ -26,6 +28,8 @@ from ._capi import (  # noqa: F401
 )
 
 PIPELINES = {"full": UW_PIPE_FULL, "exp": UW_PIPE_EXP, "pal": UW_PIPE_PAL, "direct": UW_PIPE_DIRECT}
+ACTIVATIONS = {"none": UW_ACT_NONE, "relu": UW_ACT_RELU, "silu": UW_ACT_SILU, "gelu": UW_ACT_GELU,
+               "gelu_tanh": UW_ACT_GELU_TANH}
 KERNELS = {"auto": UW_KERNEL_AUTO, "gemv": UW_KERNEL_GEMV, "mfma": UW_KERNEL_MFMA, "skinny": UW_KERNEL_SKINNY}
 
 # sections each use reads on the device
@@ -141,6 +145,48 @@ class DeviceMatrix:
             ptrs[SECTION_NAMES.index(name)] = t.data_ptr()
         self.dmat = uw_dmat()
         check(lib().uw_dmat_init(ct.byref(self.dmat), ct.byref(self.info), ptrs), "uw_dmat_init")
+
+    @classmethod
+    def from_sections(cls, rows, cols, palette, verbatim_groups, sections) -> "DeviceMatrix":
+        """A matrix whose direct-palette sections are on the device already:
+        uint8 tensors of the SM, NIB, VEXP, BITMAP and TILE_VBASE bytes, and
+        the palette's exponents in index order."""
+        torch = _torch()
+        rows, cols, verbatim_groups, palette = int(rows), int(cols), int(verbatim_groups), bytes(palette)
+        if rows < 0 or cols < 0 or cols % 64 or len(palette) > 16 or not 0 <= verbatim_groups <= rows * cols // 64:
+            raise ValueError("bad shape, palette or number of verbatim groups")
+        inf = uw_info(rows=rows, cols=cols, groups=rows * cols // 64, verbatim_groups=verbatim_groups,
+                      palette_size=len(palette), has_palette=1)
+        inf.tiles = (inf.groups + 63) // 64
+        inf.palette[:len(palette)] = palette
+        need = {"sm": rows * cols, "nib": rows * cols // 2, "vexp": 64 * verbatim_groups, "bitmap": 8 * inf.tiles,
+                "tile_vbase": 4 * (inf.tiles + 1)}
+        if set(sections) - set(need):
+            raise ValueError(f"sections of the direct-palette form are {sorted(need)}")
+        ptrs = (ct.c_void_p * UW_NUM_SECTIONS)()
+        devices = set()
+        for name, n in need.items():
+            t = sections.get(name)
+            if t is None:
+                if n:
+                    raise ValueError(f"section {name} is missing")
+                continue
+            if t.dtype != torch.uint8 or not t.is_contiguous() or not t.is_cuda or t.numel() < n:
+                raise ValueError(f"section {name}: a contiguous uint8 device tensor of at least {n} bytes is needed")
+            devices.add(t.device)
+            inf.section_bytes[SECTION_NAMES.index(name)] = n
+            ptrs[SECTION_NAMES.index(name)] = t.data_ptr()
+        if len(devices) > 1:
+            raise ValueError("the sections are on more than one device")
+        dm = cls.__new__(cls)
+        dm.info, dm.buffers, dm.dmat = inf, dict(sections), uw_dmat()
+        check(lib().uw_dmat_init(ct.byref(dm.dmat), ct.byref(inf), ptrs), "uw_dmat_init")
+        return dm
+
+    @property
+    def device(self):
+        """The device of the sections (None without any)."""
+        return next((t.device for t in self.buffers.values()), None)
 
     @property
     def rows(self):
@@ -298,6 +344,275 @@ def silu_mul_bf16(g, u, h=None, stream=None):
         h = torch.empty(g.shape, dtype=torch.bfloat16, device="cuda")
     check(lib().uw_silu_mul_bf16(_ptr(g), _ptr(u), g.numel(), _ptr(h), _stream(stream)), "uw_silu_mul_bf16")
     return h
+
+
+# ------------------------------- matmul with an epilogue, mixture of experts
+# A weight is a contiguous bf16 tensor or a DeviceMatrix with the sections of
+# the direct-palette form.  Tensors of a call are on one device, which need
+# not be the current one; the call runs on that device's current stream, or on
+# `stream` (a raw handle), where its outputs are allocated too.
+class Routing(NamedTuple):
+    """What moe_route returns: the experts and weights of every token, and its
+    slots grouped by expert (uw_moe_route)."""
+    ids: "object"
+    weights: "object"
+    offsets: "object"
+    order: "object"
+    place: "object"
+
+
+def _value_type(t, name):
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return UW_F32
+    if t.dtype == torch.bfloat16:
+        return UW_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+
+
+def _matrix_arg(t, name, rows=None, cols=None):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}], "
+                         f"not {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _x_arg(X, cols=None):
+    if X.dtype != _torch().bfloat16:
+        raise ValueError(f"X must be bfloat16, not {X.dtype}")
+    ld = _matrix_arg(X, "X", None, cols)
+    return ld if X.shape[0] > 1 else (X.shape[1] + 7) // 8 * 8
+
+
+def _index_arg(t, name, shape):
+    if t.dtype != _torch().int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)}")
+
+
+def _weight_arg(W, experts, name="W"):
+    """(bf16 pointer, descriptor, rows, cols) of one expert's matrix."""
+    if isinstance(W, DeviceMatrix):
+        n = experts or 1
+        if W.rows % n:
+            raise ValueError(f"{name}: {W.rows} rows are not {n} experts' matrices")
+        return None, ct.byref(W.dmat), W.rows // n, W.cols
+    if W.dtype != _torch().bfloat16 or not W.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bfloat16 tensor or a DeviceMatrix")
+    if W.dim() != (2 if experts is None else 3) or (experts is not None and W.shape[0] != experts):
+        raise ValueError(f"{name} must be " + ("[rows, cols]" if experts is None else f"[{experts}, rows, cols]") +
+                         f", not {list(W.shape)}")
+    return W.data_ptr(), None, W.shape[-2], W.shape[-1]
+
+
+def _one_device(first, *others):
+    """The device all of them are on (None entries are left out)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: a call takes one device")
+    return dev
+
+
+def _elsewhere(dev, stream):
+    """None where the call runs as it stands, else the context that makes
+    `dev` and `stream` the current ones."""
+    torch = _torch()
+    if stream is None:
+        return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    with torch.cuda.device(dev):
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev))
+
+
+def _out_arg(out, rows, cols, dtype, dev):
+    """(out, row stride, type), allocated where it is None."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or torch.float32, device=dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {dtype}")
+    return out, _matrix_arg(out, "out", rows, cols), _value_type(out, "out")
+
+
+def _residual_arg(residual, rows, cols):
+    if residual is None:
+        return None, UW_F32, 0
+    return residual.data_ptr(), _value_type(residual, "residual"), _matrix_arg(residual, "residual", rows, cols)
+
+
+def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None, scratch=None, stream=None):
+    """uw_linear: act(X . W^T + bias) + residual in one matmul.  W [rows, cols],
+    X bf16 [batch, cols] (any row stride that is a multiple of 8), bias [rows]
+    and residual [batch, rows] fp32 or bf16; `out` (out_dtype, fp32 by default)
+    may be the residual itself."""
+    dev = _one_device(X, W, bias, residual, out, scratch)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return linear(W, X, bias, act, residual, out, out_dtype, scratch)
+    torch = _torch()
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    w, d, rows, cols = _weight_arg(W, None)
+    ldx, batch = _x_arg(X, cols), X.shape[0]
+    if bias is not None and (bias.dim() != 1 or bias.shape[0] != rows or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous [{rows}] tensor")
+    res, res_type, ldr = _residual_arg(residual, batch, rows)
+    out, ldo, out_type = _out_arg(out, batch, rows, out_dtype, dev)
+    if scratch is None:
+        need = lib().uw_linear_scratch_bytes(rows, cols, batch)
+        if need > 0:
+            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())
+    check(lib().uw_linear(w, d, rows, cols, X.data_ptr(), ldx, batch, None if bias is None else bias.data_ptr(),
+                          UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type, ldr,
+                          out.data_ptr(), out_type, ldo, sp, sb, _stream(None)), "uw_linear")
+    return out
+
+
+def moe_route(logits, top_k, renormalize=True, scratch=None, stream=None) -> Routing:
+    """uw_moe_route: the top_k experts of every token (logits [tokens, experts],
+    fp32 or bf16), their softmax weights, and the slots grouped by expert."""
+    dev = _one_device(logits, scratch)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_route(logits, top_k, renormalize, scratch)
+    torch = _torch()
+    ld, kind = _matrix_arg(logits, "logits"), _value_type(logits, "logits")
+    tokens, experts = logits.shape
+    need = lib().uw_moe_route_scratch_bytes(tokens, experts, top_k)
+    if need < 0:
+        check(int(need), "uw_moe_route")
+    if scratch is None and need:
+        scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    i32 = torch.int32
+    r = Routing(torch.empty((tokens, top_k), dtype=i32, device=dev),
+                torch.empty((tokens, top_k), dtype=torch.float32, device=dev),
+                torch.empty(experts + 1, dtype=i32, device=dev), torch.empty(tokens * top_k, dtype=i32, device=dev),
+                torch.empty((tokens, top_k), dtype=i32, device=dev))
+    sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())
+    check(lib().uw_moe_route(logits.data_ptr(), kind, ld, tokens, experts, top_k, 1 if renormalize else 0,
+                             r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(),
+                             r.place.data_ptr(), sp, sb, _stream(None)), "uw_moe_route")
+    return r
+
+
+def _group_args(X, offsets, order):
+    """(experts, rows): the groups of a grouped matmul over X."""
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [experts + 1]")
+    _index_arg(offsets, "offsets", (offsets.shape[0],))
+    if order is None:
+        return offsets.shape[0] - 1, X.shape[0]
+    _index_arg(order, "order", (order.numel(),))
+    return offsets.shape[0] - 1, order.shape[0]
+
+
+def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, stream=None):
+    """uw_gemm_grouped: rows offsets[e] .. offsets[e+1]-1 of the result are
+    X's rows (order[s] // top_k where order is given, else s) times expert e's
+    matrix.  W [experts, rows, cols] or a DeviceMatrix of experts*rows rows."""
+    dev = _one_device(X, W, offsets, order, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return gemm_grouped(W, X, offsets, order, top_k, out, out_dtype)
+    experts, n = _group_args(X, offsets, order)
+    w, d, rows, cols = _weight_arg(W, experts)
+    ldx = _x_arg(X, cols)
+    out, ldo, out_type = _out_arg(out, n, rows, out_dtype, dev)
+    check(lib().uw_gemm_grouped(w, d, experts, rows, cols, X.data_ptr(), X.shape[0], ldx, offsets.data_ptr(),
+                                None if order is None else order.data_ptr(), top_k, n, out.data_ptr(), out_type, ldo,
+                                _stream(None)), "uw_gemm_grouped")
+    return out
+
+
+def moe_gate_up(gate, up, X, offsets, order=None, top_k=1, h=None, stream=None):
+    """uw_moe_gate_up: h = bf16(SiLU(x . gate_e^T) * (x . up_e^T)), rows and
+    inputs as gemm_grouped's."""
+    dev = _one_device(X, gate, up, offsets, order, h)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_gate_up(gate, up, X, offsets, order, top_k, h)
+    experts, n = _group_args(X, offsets, order)
+    gw, gd, rows, cols = _weight_arg(gate, experts, "gate")
+    uw_, ud, urows, ucols = _weight_arg(up, experts, "up")
+    if (urows, ucols) != (rows, cols):
+        raise ValueError("gate and up must have the same shape")
+    ldx = _x_arg(X, cols)
+    h, ldh, kind = _out_arg(h, n, rows, _torch().bfloat16, dev)
+    check(lib().uw_moe_gate_up(gw, gd, uw_, ud, experts, rows, cols, X.data_ptr(), X.shape[0], ldx, offsets.data_ptr(),
+                               None if order is None else order.data_ptr(), top_k, n, h.data_ptr(), ldh,
+                               _stream(None)), "uw_moe_gate_up")
+    return h
+
+
+def moe_combine(Y, place, weights, residual=None, out=None, out_dtype=None, stream=None):
+    """uw_moe_combine: sum_j weights[t, j] * Y[place[t, j]] (+ residual)."""
+    dev = _one_device(Y, place, weights, residual, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_combine(Y, place, weights, residual, out, out_dtype)
+    torch = _torch()
+    if Y.dtype != torch.float32 or Y.dim() != 2 or not Y.is_contiguous():
+        raise ValueError("Y must be a contiguous float32 [rows, cols] tensor")
+    if place.dim() != 2:
+        raise ValueError("place must be [tokens, top_k]")
+    _index_arg(place, "place", place.shape)
+    if weights.dtype != torch.float32 or weights.shape != place.shape or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 tensor of place's shape")
+    (tokens, top_k), (n, cols) = place.shape, Y.shape
+    res, res_type, ldr = _residual_arg(residual, tokens, cols)
+    out, ldo, out_type = _out_arg(out, tokens, cols, out_dtype, dev)
+    check(lib().uw_moe_combine(Y.data_ptr(), n, cols, place.data_ptr(), weights.data_ptr(), tokens, top_k, res,
+                               res_type, ldr, out.data_ptr(), out_type, ldo, _stream(None)), "uw_moe_combine")
+    return out
+
+
+def moe_scratch_bytes(tokens, experts, top_k, rows, cols) -> int:
+    n = lib().uw_moe_scratch_bytes(tokens, experts, top_k, rows, cols)
+    if n < 0:
+        check(int(n), "uw_moe_scratch_bytes")
+    return int(n)
+
+
+def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None, out=None, out_dtype=None,
+              scratch=None, stream=None):
+    """uw_moe_layer: sum_j w_j down_e(SiLU(gate_e x) * up_e x) over each token's
+    top_k experts (+ residual), the experts chosen by `logits`
+    [tokens, experts].  gate, up [experts, F, H] and down [experts, H, F], or
+    DeviceMatrix of experts*F and experts*H rows; `out` may be X or the
+    residual."""
+    dev = _one_device(X, gate, up, down, logits, residual, out, scratch)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_layer(gate, up, down, X, logits, top_k, renormalize, residual, out, out_dtype, scratch)
+    torch = _torch()
+    tokens, experts = X.shape[0], logits.shape[-1]
+    ldl, kind = _matrix_arg(logits, "logits", tokens), _value_type(logits, "logits")
+    gw, gd, F, H = _weight_arg(gate, experts, "gate")
+    uw_, ud, urows, ucols = _weight_arg(up, experts, "up")
+    dw, dd, drows, dcols = _weight_arg(down, experts, "down")
+    if (urows, ucols) != (F, H) or (drows, dcols) != (H, F):
+        raise ValueError("gate and up must be [experts, F, H] and down [experts, H, F]")
+    ldx = _x_arg(X, H)
+    res, res_type, ldr = _residual_arg(residual, tokens, H)
+    out, ldo, out_type = _out_arg(out, tokens, H, out_dtype, dev)
+    if scratch is None:
+        scratch = torch.empty(moe_scratch_bytes(tokens, experts, top_k, F, H), dtype=torch.uint8, device=dev)
+    check(lib().uw_moe_layer(gw, gd, uw_, ud, dw, dd, experts, F, H, X.data_ptr(), ldx, tokens, logits.data_ptr(), kind,
+                             ldl, top_k, 1 if renormalize else 0, res, res_type, ldr, out.data_ptr(), out_type, ldo,
+                             scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(None)),
+          "uw_moe_layer")
+    return out
 
 
 class KernelTimer:

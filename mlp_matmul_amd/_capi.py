@@ -22,6 +22,8 @@ SECTION_NAMES = ("sm", "stream", "glen", "tile_off", "tile_vbase", "vexp", "bitm
 UW_KERNEL_AUTO, UW_KERNEL_GEMV, UW_KERNEL_MFMA, UW_KERNEL_SKINNY = 0, 1, 2, 3
 UW_PIPE_AUTO, UW_PIPE_FULL, UW_PIPE_EXP, UW_PIPE_PAL, UW_PIPE_DIRECT, UW_PIPE_BF16, UW_PIPE_HUFF = range(7)
 UW_STATIC_SCRATCH_BYTES = 64 << 20
+UW_F32, UW_BF16 = 0, 1
+UW_ACT_NONE, UW_ACT_RELU, UW_ACT_SILU, UW_ACT_GELU, UW_ACT_GELU_TANH = range(5)
 
 
 class uw_opts(ct.Structure):
@@ -85,6 +87,17 @@ SIGNATURES = {
     "uw_mlp_scratch_bytes": (_I64, [_INT, _I64, _I64, _I64]),
     "uw_mlp_layer": (_INT, [ct.POINTER(uw_dmat), ct.POINTER(uw_dmat), ct.POINTER(uw_dmat), _INT, _P, _I64, _P, _P,
                              _U64, _P, _P]),
+    "uw_linear": (_INT, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _INT, _INT, _P, _INT, _I64, _P, _INT, _I64, _P, _U64,
+                          _P]),
+    "uw_linear_scratch_bytes": (_I64, [_I64, _I64, _I64]),
+    "uw_moe_route": (_INT, [_P, _INT, _I64, _I64, _INT, _INT, _INT, _P, _P, _P, _P, _P, _P, _U64, _P]),
+    "uw_moe_route_scratch_bytes": (_I64, [_I64, _INT, _INT]),
+    "uw_gemm_grouped": (_INT, [_P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _INT, _I64, _P]),
+    "uw_moe_gate_up": (_INT, [_P, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _I64, _P]),
+    "uw_moe_combine": (_INT, [_P, _I64, _I64, _P, _P, _I64, _INT, _P, _INT, _I64, _P, _INT, _I64, _P]),
+    "uw_moe_layer": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _INT, _I64, _INT, _INT, _P,
+                             _INT, _I64, _P, _INT, _I64, _P, _U64, _P]),
+    "uw_moe_scratch_bytes": (_I64, [_I64, _INT, _INT, _I64, _I64]),
     "uw_kernel_timer_enable": (_INT, [_INT]),
     "uw_kernel_timer_disable": (_INT, []),
     "uw_kernel_timer_reset": (_INT, []),

@@ -15,37 +15,50 @@
 #include <cstring>
 #include <string>
 
+#include "capi_common.h"
 #include "kernels.h"
 #include "uw_internal.h"
 
-namespace {
-
-int hip_fail(hipError_t e, const char* what) {
-    return uw::fail(UW_EHIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
-hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
-
-void pack_palette(const uint8_t pal[16], uint32_t out[4]) {
-    for (int i = 0; i < 4; ++i)
-        out[i] = uint32_t(pal[4 * i]) | (uint32_t(pal[4 * i + 1]) << 8) | (uint32_t(pal[4 * i + 2]) << 16) |
-                 (uint32_t(pal[4 * i + 3]) << 24);
-}
+namespace uw {
 
 int check_dmat(const uw_dmat* d, const char* who) {
-    if (!d) return uw::fail(UW_EINVAL, std::string(who) + ": NULL descriptor");
-    if (d->rows < 0 || d->cols < 0 || d->cols % uw::kGroup)
-        return uw::fail(UW_EINVAL, std::string(who) + ": bad shape");
-    if (d->groups != d->rows * d->cols / uw::kGroup || d->tiles != (d->groups + uw::kTile - 1) / uw::kTile)
-        return uw::fail(UW_EINVAL, std::string(who) + ": inconsistent descriptor sizes");
-    if (d->lmax < 0 || d->lmax > uw::kMaxCodeLen || d->palette_size < 0 || d->palette_size > 16)
-        return uw::fail(UW_EINVAL, std::string(who) + ": bad code/palette size");
+    if (!d) return fail(UW_EINVAL, std::string(who) + ": NULL descriptor");
+    if (d->rows < 0 || d->cols < 0 || d->cols % kGroup)
+        return fail(UW_EINVAL, std::string(who) + ": bad shape");
+    if (d->groups != d->rows * d->cols / kGroup || d->tiles != (d->groups + kTile - 1) / kTile)
+        return fail(UW_EINVAL, std::string(who) + ": inconsistent descriptor sizes");
+    if (d->lmax < 0 || d->lmax > kMaxCodeLen || d->palette_size < 0 || d->palette_size > 16)
+        return fail(UW_EINVAL, std::string(who) + ": bad code/palette size");
     return UW_OK;
 }
+
+int device_cus() {
+    static std::atomic<int> known[64];                 // per device, 0 until queried
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    if (dev >= 0 && dev < 64 && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    if (dev >= 0 && dev < 64) known[dev].store(cus, std::memory_order_relaxed);
+    return cus;
+}
+
+}  // namespace uw
+
+namespace {
+
+using uw::align256;
+using uw::aligned16;
+using uw::as_stream;
+using uw::check_dmat;
+using uw::device_cus;
+using uw::hip_fail;
+using uw::pack_palette;
 
 int check_decoder_inputs(const uw_dmat* d, const char* who, bool need_sm) {
     int rc = check_dmat(d, who);
@@ -92,23 +105,6 @@ int run_decode(const uw_dmat* d, void* out, int mode, void* stream, const char* 
         return uw::fail(UW_EINVAL, std::string(who) + ": output must be a 16-byte aligned device pointer");
     hipError_t e = uwk::launch_decode(mode, decode_args(d, out), as_stream(stream));
     return e == hipSuccess ? UW_OK : hip_fail(e, who);
-}
-
-// Compute units of the current device (256 if it cannot be queried).
-int device_cus() {
-    static std::atomic<int> known[64];                 // per device, 0 until queried
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess) {
-        (void)hipGetLastError();
-        return 256;
-    }
-    if (dev >= 0 && dev < 64 && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) {
-        (void)hipGetLastError();
-        return 256;
-    }
-    if (dev >= 0 && dev < 64) known[dev].store(cus, std::memory_order_relaxed);
-    return cus;
 }
 
 }  // namespace

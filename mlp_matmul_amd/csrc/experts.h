@@ -1,0 +1,82 @@
+// Argument blocks and launchers of the epilogue matmul, the products grouped
+// by expert, the router's selection and the weighted sum of the experts.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace uwk {
+
+enum ValueType { VT_F32 = 0, VT_BF16 = 1 };
+enum Activation { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4, ACT_COUNT = 5 };
+
+constexpr int kMaxExperts = 512;   // of one routed layer
+constexpr int kMaxTopK = 16;       // experts of a token
+
+// A weight: bf16 [experts, rows, cols], or the direct-palette form of
+// [experts*rows, cols] (sm not NULL).
+struct Weight {
+    const void* w;              // bf16 or 4-bit indices
+    const uint8_t* sm;
+    const uint8_t* vexp;
+    const uint64_t* bitmap;
+    const uint32_t* tile_vbase;
+    uint32_t pal[4];
+};
+
+// y = act(v + bias[r]) + residual[b][r], rounded once to the type of `out`.
+struct Epilogue {
+    const void* bias;
+    const void* residual;
+    void* out;
+    int64_t ldr, ldo;           // elements between rows of residual and out
+    int32_t bias_type, residual_type, out_type, act;
+};
+
+// One matmul (or the gate/up pair) over rows grouped by expert.
+struct GroupArgs {
+    Weight w[2];                // [1]: up of the pair
+    const uint16_t* X;
+    const int32_t* offsets;     // [E+1] first row of each expert; NULL: one group of n rows
+    const int32_t* order;       // row s reads X row order[s]/div; NULL: row s
+    int64_t ldx, x_rows, n;
+    int32_t E, R, C, div;
+    Epilogue ep;                // the pair: only out (bf16) and ldo
+    float* partial;             // [split, n, R] sums of K-slices when split > 1
+    int32_t split, cus;
+};
+
+hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s);
+
+struct RouteArgs {
+    const void* logits;
+    int64_t ld, tokens;
+    int32_t type, experts, top_k, renorm;
+    int32_t* ids;
+    float* weights;
+    int32_t* offsets;
+    int32_t* order;
+    int32_t* place;
+    int32_t* counts;            // [blocks, experts] of every block's slots, when blocks > 1
+    int32_t blocks, per_block;  // tokens of a block: a multiple of 64
+};
+
+// Blocks of tokens of a routing call (1: a single launch, no counts).
+void route_blocks(int64_t tokens, int32_t* blocks, int32_t* per_block);
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+struct CombineArgs {
+    const float* Y;             // [n, cols]
+    const int32_t* place;       // [tokens, top_k], -1: none
+    const float* weights;       // [tokens, top_k]
+    int64_t n, cols, tokens;
+    int32_t top_k;
+    const void* residual;
+    void* out;
+    int64_t ldr, ldo;
+    int32_t residual_type, out_type;
+};
+
+hipError_t launch_combine(const CombineArgs& a, hipStream_t s);
+
+}  // namespace uwk
