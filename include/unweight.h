@@ -427,9 +427,10 @@ enum {                                             /* activations, in fp32 */
 /* out[b][r] = act(sum_c X[b][c] W[r][c] + bias[r]) + residual[b][r].
  * bias [rows] and residual [batch, rows] may be NULL; out may be the residual
  * itself (same pointer, stride and type), and overlaps nothing else.
- * scratch: NULL, or uw_linear_scratch_bytes() bytes for the sums of K-slices
- * that fill the chip when batch and rows are small (without it K is not
- * split over workgroups); calls that share it must be ordered. */
+ * scratch: NULL, or uw_linear_scratch_bytes() bytes, which compressed weights
+ * use above 32 rows (sums of K-slices, or the matrix as bf16); with less than
+ * that the weights are rebuilt tile by tile, slower.  Calls that share it must
+ * be ordered.  Results with and without it agree to rounding. */
 int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols,
               const uint16_t* X, int64_t ldx, int64_t batch,
               const void* bias, int bias_type, int act,
@@ -437,8 +438,9 @@ int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols,
               void* out, int out_type, int64_t ldo,
               void* scratch, uint64_t scratch_bytes, void* stream);
 
-/* Scratch of uw_linear on the current device (>= 0, 0: none) or an error code. */
-int64_t uw_linear_scratch_bytes(int64_t rows, int64_t cols, int64_t batch);
+/* Scratch of uw_linear (compressed: whether the weight is) on the current
+ * device (>= 0, 0: none) or an error code. */
+int64_t uw_linear_scratch_bytes(int compressed, int64_t rows, int64_t cols, int64_t batch);
 
 /* The router's selection.  Of each token's `experts` logits (fp32 or bf16, row
  * stride ld) the top_k largest are chosen, equal ones by the lowest index:

@@ -89,7 +89,7 @@ SIGNATURES = {
                              _U64, _P, _P]),
     "uw_linear": (_INT, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _INT, _INT, _P, _INT, _I64, _P, _INT, _I64, _P, _U64,
                           _P]),
-    "uw_linear_scratch_bytes": (_I64, [_I64, _I64, _I64]),
+    "uw_linear_scratch_bytes": (_I64, [_INT, _I64, _I64, _I64]),
     "uw_moe_route": (_INT, [_P, _INT, _I64, _I64, _INT, _INT, _INT, _P, _P, _P, _P, _P, _P, _U64, _P]),
     "uw_moe_route_scratch_bytes": (_I64, [_I64, _INT, _INT]),
     "uw_gemm_grouped": (_INT, [_P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _INT, _I64, _P]),

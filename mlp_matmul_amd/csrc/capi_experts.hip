@@ -126,7 +126,6 @@ uwk::GroupArgs group_args(const uint16_t* X, int64_t x_rows, int64_t ldx, const 
     a.R = int32_t(rows);
     a.C = int32_t(cols);
     a.div = top_k;
-    a.split = 1;
     a.cus = uw::device_cus();
     return a;
 }
@@ -176,11 +175,15 @@ LayerLayout layer_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t
 
 extern "C" {
 
-int64_t uw_linear_scratch_bytes(int64_t rows, int64_t cols, int64_t batch) {
+int64_t uw_linear_scratch_bytes(int compressed, int64_t rows, int64_t cols, int64_t batch) {
     int64_t out = 0;
     const int rc = guarded([&]() -> int {
-        if (rows < 0 || cols < 0 || batch < 0 || cols % uw::kGroup)
-            return bad("uw_linear_scratch_bytes", "bad argument (cols must be a multiple of 64)");
+        const char* who = "uw_linear_scratch_bytes";
+        if (rows < 0 || cols < uw::kGroup || batch < 0 || batch >= (int64_t(1) << 31) || cols % uw::kGroup)
+            return bad(who, "bad argument (cols must be a positive multiple of 64)");
+        if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows * cols >= (int64_t(1) << 31))
+            return fail(UW_EUNSUPPORTED, std::string(who) + ": a matrix of 2^31 weights or more");
+        out = int64_t(uwk::linear_scratch(compressed != 0, rows, cols, batch, uw::device_cus()));
         return UW_OK;
     });
     return rc ? rc : out;
@@ -199,9 +202,11 @@ int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols, c
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {bias, residual, out, ldr, ldo, bias_type, residual_type, out_type, act};
         if ((rc = check_epilogue(a.ep, batch, rows, X, span(batch, cols, ldx, 2), who))) return rc;
-        (void)scratch;
-        (void)scratch_bytes;
-        const hipError_t e = uwk::launch_grouped(d != nullptr, false, a, as_stream(stream));
+        if (!aligned16(scratch)) return bad(who, "misaligned scratch");
+        if (!scratch) scratch_bytes = 0;
+        if (overlap(out, span(batch, rows, ldo, value_bytes(out_type)), scratch, scratch_bytes))
+            return bad(who, "out overlaps the scratch");
+        const hipError_t e = uwk::launch_linear(d != nullptr, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
 }

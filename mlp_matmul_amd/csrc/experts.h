@@ -42,11 +42,26 @@ struct GroupArgs {
     int64_t ldx, x_rows, n;
     int32_t E, R, C, div;
     Epilogue ep;                // the pair: only out (bf16) and ldo
-    float* partial;             // [split, n, R] sums of K-slices when split > 1
-    int32_t split, cus;
+    int32_t cus;
 };
 
+// Scratch of the epilogue matmul (0: none is used).
+uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int cus);
+// The epilogue matmul: a.n rows of X in order, no offsets.
+hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s);
+// A product grouped by expert, or the gate/up pair.
 hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s);
+
+// The kernels behind them.  One or two rows an expert, cols <= 24576 / rows:
+bool gemv_rows_supported(const GroupArgs& a, int nb);
+hipError_t launch_gemv_rows(bool pal, bool pair, const GroupArgs& a, int nb, hipStream_t s);
+// Up to `rows` (4, 16 or 32) rows an expert before its weights are read again.
+hipError_t launch_skinny_rows(bool pal, bool pair, const GroupArgs& a, int rows, hipStream_t s);
+// Tiles of weight rows x input rows, bf16 and palette.
+enum TileShape { TILE_64x64, TILE_128x64, TILE_256x128, TILE_256x256, TILE_SHAPES };
+hipError_t launch_tile(bool pair, const GroupArgs& a, TileShape shape, hipStream_t s);
+enum PalTileShape { PAL_TILE_64x64, PAL_TILE_128x64, PAL_TILE_128x128 };
+hipError_t launch_tile_pal(bool pair, const GroupArgs& a, PalTileShape shape, hipStream_t s);
 
 struct RouteArgs {
     const void* logits;

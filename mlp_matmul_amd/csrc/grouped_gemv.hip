@@ -1,0 +1,299 @@
+// One or two rows per expert (a single token, or a batch of one or two of the
+// epilogue matmul): the weight stream bounds the product, there is nothing to
+// reuse, so a weight goes from memory to registers, is rebuilt there and
+// multiplied with v_dot2 (two bf16 products, fp32 sum).
+//
+// A wave owns whole rows of the expert's matrix (of gate and up: the same row
+// of both) and walks them in slabs of 1024 columns, 16 a lane; every load
+// instruction reads one contiguous run.  The items (row, slab) run through a
+// ring of D register sets: D items are in flight, the loop has no branch
+// around a load.  The input rows are staged in LDS once per workgroup of four
+// waves.  A row's 64 lane sums are added by a butterfly: the order is fixed.
+// Verbatim groups: a wave keeps the bitmap word and the base of every tile its
+// rows touch, one tile a lane; an item picks its 16 flags by lane reads, so
+// flags and slots cost scalar instructions, and the raw exponents come with
+// the item's other loads (lanes outside verbatim groups share one line).
+#include "grouped_common.h"
+#include "kernels.h"
+
+namespace uwk {
+
+namespace {
+
+constexpr int kSlab = 1024;
+constexpr int kGemvWaves = 4;
+
+template <bool PAL>
+struct Item {
+    u32x4_t a, b;       // bf16: the halves; palette: a.xy indices, b sign/mantissa
+    u32x4_t vx;         // palette: raw exponents
+    uint32_t verb;
+};
+
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int l) {
+    return (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), l))) << 32) |
+           uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), l));
+}
+
+template <bool PAL, bool PAIR, int NB, int D>
+__global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a, uint32_t bands, int rows_per_wave) {
+    constexpr int M = PAIR ? 2 : 1;
+    __shared__ uint32_t lut[PAL ? 256 * M : 1];
+    extern __shared__ __align__(16) uint16_t xs[];           // [NB][slabs * 1024]
+    GroupTile t;
+    if (!group_tile<NB>(a, bands, t)) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t R = uint32_t(a.R), C = uint32_t(a.C), slabs = (C + kSlab - 1) / kSlab;
+    const uint32_t r0 = (uint32_t(t.band) * kGemvWaves + uint32_t(wave)) * uint32_t(rows_per_wave);
+    // a wave past the matrix walks its last row and stores nothing
+    const uint32_t my_rows = r0 < R ? min(uint32_t(rows_per_wave), R - r0) : 0u;
+    const uint32_t rl = min(r0, R - 1u), total = max(my_rows, 1u) * slabs * M;
+    const int64_t first = int64_t(t.e) * R * C;
+
+    // verbatim tables of the wave's rows
+    const int64_t g0 = (first + int64_t(rl) * C) >> 6;       // the first row's first group
+    const int64_t t0 = g0 >> 6;
+    uint64_t word[M];
+    uint32_t base[M], ebase[M];
+    if (PAL) {
+        const int64_t tl = (g0 + int64_t(max(my_rows, 1u)) * (C >> 6) - 1) >> 6;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            word[m] = a.w[m].bitmap[min(t0 + lane, tl)];
+            base[m] = a.w[m].tile_vbase[min(t0 + lane, tl)];
+            ebase[m] = a.w[m].tile_vbase[first >> 12];
+        }
+    }
+    float bias = 0.f, residual[NB] = {};                     // of the next row to finish; lane 0 uses them
+
+    struct Pos {
+        uint32_t row, m, s;                                  // row from rl, matrix, slab
+    };
+    auto next = [&](Pos p) -> Pos {
+        if (p.s + 1 < slabs) return {p.row, p.m, p.s + 1};
+        if (PAIR && p.m == 0) return {p.row, 1u, 0u};
+        return {p.row + 1, 0u, 0u};
+    };
+    const uint32_t lane16 = uint32_t(lane) * 16u;
+    auto issue = [&](Pos p, Item<PAL>& it) {
+        const Weight& w = PAIR && p.m ? a.w[M - 1] : a.w[0];
+        const uint64_t pos = uint64_t(first) + uint64_t(rl + p.row) * C + p.s * kSlab;   // uniform
+        const uint32_t left = C - p.s * kSlab;               // columns of the slab, 1024 or fewer
+        if (!PAL) {
+            const uint16_t* const b = static_cast<const uint16_t*>(w.w) + pos;
+            const uint32_t k0 = uint32_t(lane) * 8u, k1 = 512u + k0;
+            it.a = load_stream16(b + (k0 < left ? k0 : 0u));
+            it.b = load_stream16(b + (k1 < left ? k1 : 0u));
+            return;
+        }
+        const uint32_t k = lane16 < left ? lane16 : 0u;
+        const u32x2_t n = load_stream8(static_cast<const uint8_t*>(w.w) + pos / 2 + k / 2);
+        it.a = u32x4_t{n[0], n[1], 0u, 0u};
+        it.b = load_stream16(w.sm + pos + k);
+        // flags of the slab's 16 groups: uniform
+        const uint32_t gi = uint32_t(int64_t(pos >> 6) - (t0 << 6)), tl = gi >> 6, gb = gi & 63u;
+        const uint64_t mw = PAIR && p.m ? word[M - 1] : word[0];
+        const uint32_t mb = PAIR && p.m ? base[M - 1] : base[0];
+        const uint64_t w0 = readlane64(mw, int(tl));
+        uint64_t bits = w0 >> gb;
+        if (gb > 48u) bits |= readlane64(mw, int(min(tl + 1u, 63u))) << (64u - gb);
+        // groups behind the row's end are other rows' (clamped lanes look at group 0)
+        const uint32_t m16 = uint32_t(bits) & 0xFFFFu;
+        const uint32_t start = uint32_t(__builtin_amdgcn_readlane(int(mb), int(tl))) -
+                               (PAIR && p.m ? ebase[M - 1] : ebase[0]) +
+                               uint32_t(__popcll(gb ? w0 & ((uint64_t(1) << gb) - 1) : 0));
+        const uint32_t grp = k >> 6;
+        it.verb = (m16 >> grp) & 1u;
+        const uint32_t slot = start + uint32_t(__popc(m16 & ((1u << grp) - 1u)));
+        const uint8_t* const vb = w.vexp + uint64_t(PAIR && p.m ? ebase[M - 1] : ebase[0]) * 64u;
+        it.vx = load16(vb + (it.verb ? slot * 64u + (k & 63u) : 0u));
+    };
+
+    constexpr int NS = D + 1;                                // register sets: D items in flight past the one computed
+    Item<PAL> ring[NS];
+    Pos at[NS], last{0, 0, 0};
+    // loads first: the input rows' addresses and the tables wait for other loads
+    if (!PAL) {
+        Pos p{0, 0, 0};
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (d > 0 && uint32_t(d) < total) p = next(p);
+            at[d] = p;
+            issue(p, ring[d]);
+        }
+        last = p;
+    }
+    if (PAL) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            lut[256 * m + tid] = (pal_byte(a.w[m].pal, uint32_t(tid) & 15u) << 7) |
+                                 (pal_byte(a.w[m].pal, uint32_t(tid) >> 4) << 23);
+    }
+    // input rows to LDS, zeros behind C; palette: the two halves of a lane's 16
+    // columns 64 chunks apart, so that both are conflict-free 16-byte reads
+    const uint32_t chunks = C / 8u, all = slabs * (kSlab / 8);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint16_t* const x = group_x_row(a, t.row0 + (b < t.rows ? b : 0));
+        for (uint32_t c = uint32_t(tid); c < all; c += 64u * kGemvWaves) {
+            const u32x4_t v = c < chunks ? load16(x + c * 8u) : u32x4_t{0u, 0u, 0u, 0u};
+            const uint32_t in = c & 127u, to = PAL ? (c & ~127u) + (in & 1u) * 64u + (in >> 1) : c;
+            store16(xs + (uint32_t(b) * all + to) * 8u, v);
+        }
+    }
+    if (PAL) {
+        Pos p{0, 0, 0};
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (d > 0 && uint32_t(d) < total) p = next(p);
+            at[d] = p;
+            issue(p, ring[d]);
+        }
+        last = p;
+    }
+    auto load_ends = [&](uint32_t row) {
+        const uint32_t r = min(rl + row, R - 1u);
+        if (a.ep.bias)
+            bias = a.ep.bias_type == VT_F32 ? static_cast<const float*>(a.ep.bias)[r]
+                                            : bf16_value(static_cast<const uint16_t*>(a.ep.bias)[r]);
+        if (a.ep.residual) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int64_t o = (t.row0 + (b < t.rows ? b : 0)) * a.ep.ldr + r;
+                residual[b] = a.ep.residual_type == VT_F32 ? static_cast<const float*>(a.ep.residual)[o]
+                                                           : bf16_value(static_cast<const uint16_t*>(a.ep.residual)[o]);
+            }
+        }
+    };
+    if (!PAIR) load_ends(0);
+    __syncthreads();
+
+    float acc[NB], gate[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = gate[b] = 0.f;
+
+    auto compute = [&](Pos p, const Item<PAL>& it) {
+        uint32_t w[8];
+        if (!PAL) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = it.a[i];
+                w[4 + i] = it.b[i];
+            }
+        } else {
+            const char* const l = reinterpret_cast<const char*>(lut) + (PAIR && p.m ? 1024u : 0u);
+            uint32_t e7[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                e7[i] = *reinterpret_cast<const uint32_t*>(l + (((it.a[i >> 2] >> (8 * (i & 3))) & 0xFFu) << 2));
+            if (__builtin_amdgcn_ballot_w64(it.verb != 0)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t raw = (i & 1) ? exp_pair<1>(it.vx[i >> 1]) : exp_pair<0>(it.vx[i >> 1]);
+                    e7[i] = it.verb ? raw : e7[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = (i & 1) ? join_pair<1>(it.b[i >> 1], e7[i]) : join_pair<0>(it.b[i >> 1], e7[i]);
+        }
+        const uint32_t left = C - p.s * kSlab;
+        if (left < uint32_t(kSlab)) {                        // columns behind C: zeros by zeros
+            const bool z0 = PAL ? lane16 >= left : uint32_t(lane) * 8u >= left;
+            const bool z1 = PAL ? z0 : 512u + uint32_t(lane) * 8u >= left;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = z0 ? 0u : w[i];
+                w[4 + i] = z1 ? 0u : w[4 + i];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint16_t* const x = xs + (uint32_t(b) * all + p.s * 128u + uint32_t(lane)) * 8u;
+            const u32x4_t x0 = load16(x), x1 = load16(x + 512);
+            float s = acc[b];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = dot2_bf16(w[i], x0[i], s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = dot2_bf16(w[4 + i], x1[i], s);
+            acc[b] = s;
+        }
+        if (p.s + 1 < slabs) return;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float v = wave_sum(acc[b]);
+            acc[b] = 0.f;
+            if (PAIR) {
+                if (p.m == 0) {
+                    gate[b] = v;
+                    continue;
+                }
+                v = silu_mul1(gate[b], v);
+            }
+            if (lane == 0 && b < t.rows && p.row < my_rows) {
+                if (a.ep.bias) v += bias;
+                v = activate(v, a.ep.act);
+                if (a.ep.residual) v += residual[b];
+                const int64_t o = (t.row0 + b) * a.ep.ldo + r0 + p.row;
+                if (a.ep.out_type == VT_BF16) static_cast<uint16_t*>(a.ep.out)[o] = uint16_t(f32_to_bf16_rne(v));
+                else static_cast<float*>(a.ep.out)[o] = v;
+            }
+        }
+        if (!PAIR && p.row + 1 < my_rows) load_ends(p.row + 1);
+    };
+
+    uint32_t done = 0;
+    for (; done + NS <= total; done += NS) {
+#pragma unroll
+        for (int d = 0; d < NS; ++d) {
+            // items past the end read the last one again
+            if (done + uint32_t(d) + D < total) last = next(last);
+            at[(d + D) % NS] = last;
+            issue(last, ring[(d + D) % NS]);
+            compute(at[d], ring[d]);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < NS - 1; ++d)
+        if (done + uint32_t(d) < total) compute(at[d], ring[d]);
+}
+
+// Rows of a wave: one, or two on tall matrices (a wave's start is paid for half
+// as often; single matrices only, 65536 x 4096: 65 us against 77), as long as
+// the tables of its tiles fit its lanes.
+int rows_of_wave(const GroupArgs& a, bool pair) {
+    return !pair && a.R >= 8192 && 2 * int64_t(a.C) <= 60 * 4096 ? 2 : 1;
+}
+
+size_t staged_bytes(const GroupArgs& a, int nb) { return size_t(nb) * ((a.C + kSlab - 1) / kSlab) * kSlab * 2; }
+
+// Two items in flight; one for the palette pair and for two input rows, where
+// the registers of the second cost more waves than it gains (palette pair, two
+// experts of 3584 x 4096: 20.0 us against 21.9).
+template <bool PAL, bool PAIR, int NB>
+hipError_t launch(const GroupArgs& a, hipStream_t s) {
+    constexpr int D = NB > 1 || (PAL && PAIR) ? 1 : 2;
+    const int rpw = rows_of_wave(a, PAIR);
+    const int64_t bands = (a.R + kGemvWaves * rpw - 1) / (kGemvWaves * rpw);
+    const int64_t units = group_units(a, NB, bands);
+    if (units > 0x7FFFFFFF) return hipErrorInvalidValue;
+    launch_timed(gemv_rows_kernel<PAL, PAIR, NB, D>, dim3(unsigned(units)), dim3(64 * kGemvWaves), staged_bytes(a, NB),
+                 s, a, uint32_t(bands), rpw);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// The input rows fit 48 KB of LDS and a wave's tiles its 64 lanes.
+bool gemv_rows_supported(const GroupArgs& a, int nb) { return staged_bytes(a, nb) <= 48 * 1024; }
+
+hipError_t launch_gemv_rows(bool pal, bool pair, const GroupArgs& a, int nb, hipStream_t s) {
+    if (nb == 1)
+        return pal ? (pair ? launch<true, true, 1>(a, s) : launch<true, false, 1>(a, s))
+                   : (pair ? launch<false, true, 1>(a, s) : launch<false, false, 1>(a, s));
+    return pal ? (pair ? launch<true, true, 2>(a, s) : launch<true, false, 2>(a, s))
+               : (pair ? launch<false, true, 2>(a, s) : launch<false, false, 2>(a, s));
+}
+
+}  // namespace uwk

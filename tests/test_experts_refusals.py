@@ -64,7 +64,7 @@ BAD = {
     linear: [dict(w=None), dict(w=at(1) + 2), dict(cols=100), dict(cols=0), dict(rows=-1), dict(batch=-1),
              dict(ldx=255), dict(ldx=260), dict(X=None), dict(X=at(2) + 4), dict(bt=2), dict(bias=at(3) + 2),
              dict(act=5), dict(act=-1), dict(rt=7), dict(ldr=127), dict(ot=2), dict(out=None), dict(out=at(5) + 4),
-             dict(ldo=127), dict(out=at(2) + 256), dict(out=at(3)), dict(out=at(4) + 16), dict(out=at(4), ot=1),
+             dict(ldo=127), dict(scratch=at(9) + 4, sb=64), dict(scratch=at(5), sb=1 << 20), dict(out=at(2) + 256), dict(out=at(3)), dict(out=at(4) + 16), dict(out=at(4), ot=1),
              dict(out=at(4), ldo=130), dict(batch=1 << 31)],
     route: [dict(tokens=-1), dict(experts=0), dict(experts=513), dict(top_k=0), dict(top_k=9), dict(lt=3),
             dict(ld=7), dict(logits=None), dict(ids=None), dict(weights=at(3) + 4), dict(off=None), dict(order=None),
@@ -140,8 +140,12 @@ def test_scratch_sizes():
     assert L.uw_moe_route_scratch_bytes(1, 0, 1) == _capi.UW_EINVAL
     assert L.uw_moe_scratch_bytes(3, 8, 2, 64, 128) == 256 * 5 + 6 * 64 * 2 + 6 * 128 * 4
     assert L.uw_moe_scratch_bytes(3, 8, 2, 60, 128) == _capi.UW_EINVAL
-    assert L.uw_linear_scratch_bytes(64, 100, 4) == _capi.UW_EINVAL
-    assert L.uw_linear_scratch_bytes(4096, 4096, 1) >= 0
+    assert L.uw_linear_scratch_bytes(1, 64, 100, 4) == _capi.UW_EINVAL
+    assert L.uw_linear_scratch_bytes(1, 1 << 20, 1 << 11, 4) == _capi.UW_EUNSUPPORTED
+    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 32) == 0
+    assert L.uw_linear_scratch_bytes(0, 4096, 4096, 5000) == 0
+    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 5000) == 2 * 4096 * 4096
+    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 100) % (100 * 4096 * 4) == 0
 
 
 def test_from_sections_refusals():
