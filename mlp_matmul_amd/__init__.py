@@ -418,6 +418,12 @@ def _one_device(first, *others):
     return dev
 
 
+def _current_stream(dev):
+    """Raw handle of the device's current stream (without the Stream object
+    that torch.cuda.current_stream makes: 2.7 us a call)."""
+    return _torch()._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _elsewhere(dev, stream):
     """None where the call runs as it stands, else the context that makes
     `dev` and `stream` the current ones."""
@@ -432,8 +438,10 @@ def _out_arg(out, rows, cols, dtype, dev):
     """(out, row stride, type), allocated where it is None."""
     torch = _torch()
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype or torch.float32, device=dev)
-    elif dtype is not None and out.dtype != dtype:
+        dtype = dtype or torch.float32
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        return out, max(cols, 1), _value_type(out, "out")
+    if dtype is not None and out.dtype != dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {dtype}")
     return out, _matrix_arg(out, "out", rows, cols), _value_type(out, "out")
 
@@ -470,7 +478,7 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())
     check(lib().uw_linear(w, d, rows, cols, X.data_ptr(), ldx, batch, None if bias is None else bias.data_ptr(),
                           UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type, ldr,
-                          out.data_ptr(), out_type, ldo, sp, sb, _stream(None)), "uw_linear")
+                          out.data_ptr(), out_type, ldo, sp, sb, _current_stream(dev)), "uw_linear")
     return out
 
 
@@ -498,7 +506,7 @@ def moe_route(logits, top_k, renormalize=True, scratch=None, stream=None) -> Rou
     sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())
     check(lib().uw_moe_route(logits.data_ptr(), kind, ld, tokens, experts, top_k, 1 if renormalize else 0,
                              r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(),
-                             r.place.data_ptr(), sp, sb, _stream(None)), "uw_moe_route")
+                             r.place.data_ptr(), sp, sb, _current_stream(dev)), "uw_moe_route")
     return r
 
 
@@ -528,7 +536,7 @@ def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, s
     out, ldo, out_type = _out_arg(out, n, rows, out_dtype, dev)
     check(lib().uw_gemm_grouped(w, d, experts, rows, cols, X.data_ptr(), X.shape[0], ldx, offsets.data_ptr(),
                                 None if order is None else order.data_ptr(), top_k, n, out.data_ptr(), out_type, ldo,
-                                _stream(None)), "uw_gemm_grouped")
+                                _current_stream(dev)), "uw_gemm_grouped")
     return out
 
 
@@ -549,7 +557,7 @@ def moe_gate_up(gate, up, X, offsets, order=None, top_k=1, h=None, stream=None):
     h, ldh, kind = _out_arg(h, n, rows, _torch().bfloat16, dev)
     check(lib().uw_moe_gate_up(gw, gd, uw_, ud, experts, rows, cols, X.data_ptr(), X.shape[0], ldx, offsets.data_ptr(),
                                None if order is None else order.data_ptr(), top_k, n, h.data_ptr(), ldh,
-                               _stream(None)), "uw_moe_gate_up")
+                               _current_stream(dev)), "uw_moe_gate_up")
     return h
 
 
@@ -572,7 +580,7 @@ def moe_combine(Y, place, weights, residual=None, out=None, out_dtype=None, stre
     res, res_type, ldr = _residual_arg(residual, tokens, cols)
     out, ldo, out_type = _out_arg(out, tokens, cols, out_dtype, dev)
     check(lib().uw_moe_combine(Y.data_ptr(), n, cols, place.data_ptr(), weights.data_ptr(), tokens, top_k, res,
-                               res_type, ldr, out.data_ptr(), out_type, ldo, _stream(None)), "uw_moe_combine")
+                               res_type, ldr, out.data_ptr(), out_type, ldo, _current_stream(dev)), "uw_moe_combine")
     return out
 
 
@@ -610,7 +618,7 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
         scratch = torch.empty(moe_scratch_bytes(tokens, experts, top_k, F, H), dtype=torch.uint8, device=dev)
     check(lib().uw_moe_layer(gw, gd, uw_, ud, dw, dd, experts, F, H, X.data_ptr(), ldx, tokens, logits.data_ptr(), kind,
                              ldl, top_k, 1 if renormalize else 0, res, res_type, ldr, out.data_ptr(), out_type, ldo,
-                             scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(None)),
+                             scratch.data_ptr(), scratch.numel() * scratch.element_size(), _current_stream(dev)),
           "uw_moe_layer")
     return out
 

@@ -302,8 +302,8 @@ int uw_moe_combine(const float* Y, int64_t n, int64_t cols, const int32_t* place
         const uwk::Epilogue ep{nullptr, residual, out, ldr, ldo, UW_F32, residual_type, out_type, UW_ACT_NONE};
         int rc = check_epilogue(ep, tokens, cols, Y, span(n, cols, cols, 4), who);
         if (rc) return rc;
-        const uwk::CombineArgs a{Y, place, weights, n, cols, tokens, top_k, residual, out, ldr, ldo, residual_type,
-                                 out_type};
+        const uwk::CombineArgs a{Y, place, nullptr, weights, n, cols, tokens, top_k, residual, out, ldr, ldo,
+                                 residual_type, out_type};
         const hipError_t e = uwk::launch_combine(a, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
@@ -335,10 +335,10 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         if (rc) return rc;
         if (rows < uw::kGroup || cols < uw::kGroup || rows % uw::kGroup || cols % uw::kGroup)
             return bad(who, "gate and up are [rows, cols], down [cols, rows], rows and cols positive multiples of 64");
-        uwk::Weight probe;
+        uwk::Weight probe, down;
         if ((rc = take_weight(gate_w, gate_d, experts, rows, cols, &probe, who)) ||
             (rc = take_weight(up_w, up_d, experts, rows, cols, &probe, who)) ||
-            (rc = take_weight(down_w, down_d, experts, cols, rows, &probe, who)))
+            (rc = take_weight(down_w, down_d, experts, cols, rows, &down, who)))
             return rc;
         if ((gate_d != nullptr) != (up_d != nullptr)) return bad(who, "gate and up must both be bf16 or both compressed");
         if (tokens == 0) return UW_OK;
@@ -368,6 +368,16 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         if ((rc = uw_moe_gate_up(gate_w, gate_d, up_w, up_d, experts, rows, cols, X, tokens, ldx, offsets, order,
                                  top_k, n, h, rows, stream)))
             return rc;
+        if (tokens == 1) {                      // a single token's sum needs no array of the experts' outputs
+            uwk::GroupArgs a = group_args(h, n, rows, offsets, nullptr, 1, n, experts, cols, rows);
+            a.w[0] = down;
+            if (uwk::gemv_combine_supported(a, top_k)) {
+                const uwk::CombineArgs c{nullptr, place, ids, weights, n, cols, 1, top_k, residual, out, ldr, ldo,
+                                         residual_type, out_type};
+                const hipError_t e = uwk::launch_gemv_combine(down_d != nullptr, a, c, as_stream(stream));
+                return e == hipSuccess ? UW_OK : hip_fail(e, who);
+            }
+        }
         if ((rc = uw_gemm_grouped(down_w, down_d, experts, cols, rows, h, n, rows, offsets, nullptr, 1, n, y, UW_F32,
                                   cols, stream)))
             return rc;

@@ -45,6 +45,19 @@ struct GroupArgs {
     int32_t cus;
 };
 
+struct CombineArgs {
+    const float* Y;             // [n, cols]
+    const int32_t* place;       // [tokens, top_k], -1: none
+    const int32_t* ids;         // [tokens, top_k] (launch_gemv_combine)
+    const float* weights;       // [tokens, top_k]
+    int64_t n, cols, tokens;
+    int32_t top_k;
+    const void* residual;
+    void* out;
+    int64_t ldr, ldo;
+    int32_t residual_type, out_type;
+};
+
 // Scratch of the epilogue matmul (0: none is used).
 uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int cus);
 // The epilogue matmul: a.n rows of X in order, no offsets.
@@ -55,6 +68,10 @@ hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s
 // The kernels behind them.  One or two rows an expert, cols <= 24576 / rows:
 bool gemv_rows_supported(const GroupArgs& a, int nb);
 hipError_t launch_gemv_rows(bool pal, bool pair, const GroupArgs& a, int nb, hipStream_t s);
+// One token's down projection and the weighted sum of its experts (c.Y is not
+// read): a.X the rows that c.place names.
+bool gemv_combine_supported(const GroupArgs& a, int top_k);
+hipError_t launch_gemv_combine(bool pal, const GroupArgs& a, const CombineArgs& c, hipStream_t s);
 // Up to `rows` (4, 16 or 32) rows an expert before its weights are read again.
 hipError_t launch_skinny_rows(bool pal, bool pair, const GroupArgs& a, int rows, hipStream_t s);
 // Tiles of weight rows x input rows, bf16 and palette.
@@ -79,18 +96,6 @@ struct RouteArgs {
 // Blocks of tokens of a routing call (1: a single launch, no counts).
 void route_blocks(int64_t tokens, int32_t* blocks, int32_t* per_block);
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
-
-struct CombineArgs {
-    const float* Y;             // [n, cols]
-    const int32_t* place;       // [tokens, top_k], -1: none
-    const float* weights;       // [tokens, top_k]
-    int64_t n, cols, tokens;
-    int32_t top_k;
-    const void* residual;
-    void* out;
-    int64_t ldr, ldo;
-    int32_t residual_type, out_type;
-};
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s);
 

@@ -35,6 +35,55 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int l) {
            uint32_t(__builtin_amdgcn_readlane(int(uint32_t(v)), l));
 }
 
+// The item's 16 weights as bf16 pairs; `lut` maps two indices to both exponents in place.
+template <bool PAL>
+__device__ __forceinline__ void item_weights(const Item<PAL>& it, const char* lut, uint32_t w[8]) {
+    if (!PAL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = it.a[i];
+            w[4 + i] = it.b[i];
+        }
+        return;
+    }
+    uint32_t e7[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        e7[i] = *reinterpret_cast<const uint32_t*>(lut + (((it.a[i >> 2] >> (8 * (i & 3))) & 0xFFu) << 2));
+    if (__builtin_amdgcn_ballot_w64(it.verb != 0)) {         // rare: raw exponents for verbatim lanes
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t raw = (i & 1) ? exp_pair<1>(it.vx[i >> 1]) : exp_pair<0>(it.vx[i >> 1]);
+            e7[i] = it.verb ? raw : e7[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = (i & 1) ? join_pair<1>(it.b[i >> 1], e7[i]) : join_pair<0>(it.b[i >> 1], e7[i]);
+}
+
+// Zeros for the columns from `left` on of a slab (their inputs are zeros too).
+template <bool PAL>
+__device__ __forceinline__ void cut_weights(uint32_t left, int lane, uint32_t w[8]) {
+    const bool z0 = PAL ? uint32_t(lane) * 16u >= left : uint32_t(lane) * 8u >= left;
+    const bool z1 = PAL ? z0 : 512u + uint32_t(lane) * 8u >= left;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = z0 ? 0u : w[i];
+        w[4 + i] = z1 ? 0u : w[4 + i];
+    }
+}
+
+// s plus the item's products with the staged inputs of its two halves.
+__device__ __forceinline__ float item_dot(const uint32_t w[8], const uint16_t* x, float s) {
+    const u32x4_t x0 = load16(x), x1 = load16(x + 512);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = dot2_bf16(w[i], x0[i], s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = dot2_bf16(w[4 + i], x1[i], s);
+    return s;
+}
+
 template <bool PAL, bool PAIR, int NB, int D>
 __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a, uint32_t bands, int rows_per_wave) {
     constexpr int M = PAIR ? 2 : 1;
@@ -175,50 +224,12 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a,
 
     auto compute = [&](Pos p, const Item<PAL>& it) {
         uint32_t w[8];
-        if (!PAL) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = it.a[i];
-                w[4 + i] = it.b[i];
-            }
-        } else {
-            const char* const l = reinterpret_cast<const char*>(lut) + (PAIR && p.m ? 1024u : 0u);
-            uint32_t e7[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                e7[i] = *reinterpret_cast<const uint32_t*>(l + (((it.a[i >> 2] >> (8 * (i & 3))) & 0xFFu) << 2));
-            if (__builtin_amdgcn_ballot_w64(it.verb != 0)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t raw = (i & 1) ? exp_pair<1>(it.vx[i >> 1]) : exp_pair<0>(it.vx[i >> 1]);
-                    e7[i] = it.verb ? raw : e7[i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = (i & 1) ? join_pair<1>(it.b[i >> 1], e7[i]) : join_pair<0>(it.b[i >> 1], e7[i]);
-        }
+        item_weights<PAL>(it, reinterpret_cast<const char*>(lut) + (PAIR && p.m ? 1024u : 0u), w);
         const uint32_t left = C - p.s * kSlab;
-        if (left < uint32_t(kSlab)) {                        // columns behind C: zeros by zeros
-            const bool z0 = PAL ? lane16 >= left : uint32_t(lane) * 8u >= left;
-            const bool z1 = PAL ? z0 : 512u + uint32_t(lane) * 8u >= left;
+        if (left < uint32_t(kSlab)) cut_weights<PAL>(left, lane, w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = z0 ? 0u : w[i];
-                w[4 + i] = z1 ? 0u : w[4 + i];
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const uint16_t* const x = xs + (uint32_t(b) * all + p.s * 128u + uint32_t(lane)) * 8u;
-            const u32x4_t x0 = load16(x), x1 = load16(x + 512);
-            float s = acc[b];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s = dot2_bf16(w[i], x0[i], s);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s = dot2_bf16(w[4 + i], x1[i], s);
-            acc[b] = s;
-        }
+        for (int b = 0; b < NB; ++b)
+            acc[b] = item_dot(w, xs + (uint32_t(b) * all + p.s * 128u + uint32_t(lane)) * 8u, acc[b]);
         if (p.s + 1 < slabs) return;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -259,6 +270,138 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a,
         if (done + uint32_t(d) < total) compute(at[d], ring[d]);
 }
 
+// One token's down projection with the weighted sum of its experts:
+//   out[r] = sum_j weights[j] * (D_e(j)[r] . h[place[j]]) (+ residual[r])
+// A wave owns an output row and walks that row of every chosen expert's matrix
+// in turn, so the sum stays in its registers: no array of the experts' outputs
+// and no launch that adds it.  Items, ring and rebuild as above; lane j*tiles +
+// i keeps the verbatim word and base of tile i of expert j's row.
+template <bool PAL, int D>
+__global__ __launch_bounds__(64 * kGemvWaves) void gemv_combine_kernel(GroupArgs a, CombineArgs c) {
+    __shared__ uint32_t lut[PAL ? 256 : 1];
+    extern __shared__ __align__(16) uint16_t xs[];           // [chosen][slabs * 1024]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t R = uint32_t(a.R), C = uint32_t(a.C), slabs = (C + kSlab - 1) / kSlab;
+    const uint32_t row = min(blockIdx.x * kGemvWaves + uint32_t(wave), R - 1u);
+    const bool mine = blockIdx.x * kGemvWaves + uint32_t(wave) < R;
+
+    // the chosen experts, in lane j; those without one come last
+    const int32_t lj = min(lane, c.top_k - 1);
+    const int32_t id = c.ids[lj], pl = c.place[lj];
+    const float wt = c.weights[lj];
+    const bool real = lane < c.top_k && id >= 0 && id < a.E && pl >= 0 && pl < c.n;
+    const uint64_t some = __builtin_amdgcn_ballot_w64(real);
+    const uint32_t chosen = uint32_t(__builtin_ctzll(~some)), total = chosen * slabs;
+    auto expert = [&](uint32_t j) -> uint32_t { return uint32_t(__builtin_amdgcn_readlane(id, int(j))); };
+    auto first_of = [&](uint32_t e) -> uint64_t { return uint64_t(e) * R * C; };
+
+    const Weight& w = a.w[0];
+    const uint32_t tiles = (C + 4095) / 4096 + 1;            // of a row, at most
+    uint64_t word = 0;
+    uint32_t base = 0, ebase = 0;
+    if (PAL) {
+        const uint32_t j = min(uint32_t(lane) / tiles, uint32_t(c.top_k) - 1u);
+        const int32_t ej = __shfl(id, int(j));
+        const uint64_t g = (first_of(uint32_t(ej < 0 || ej >= a.E ? 0 : ej)) + uint64_t(row) * C) >> 6;
+        const uint64_t tl = min((g >> 6) + uint32_t(lane) % tiles, (g + (C >> 6) - 1) >> 6);
+        word = w.bitmap[tl];
+        base = w.tile_vbase[tl];
+        ebase = w.tile_vbase[first_of(uint32_t(id < 0 || id >= a.E ? 0 : id)) >> 12];   // lane j: expert j's
+        lut[tid] = (pal_byte(w.pal, uint32_t(tid) & 15u) << 7) | (pal_byte(w.pal, uint32_t(tid) >> 4) << 23);
+    }
+    struct Pos {
+        uint32_t j, s;
+    };
+    auto next = [&](Pos p) -> Pos { return p.s + 1 < slabs ? Pos{p.j, p.s + 1} : Pos{p.j + 1, 0u}; };
+    const uint32_t lane16 = uint32_t(lane) * 16u;
+    auto issue = [&](Pos p, Item<PAL>& it) {
+        const uint64_t pos = first_of(expert(p.j)) + uint64_t(row) * C + p.s * kSlab;    // uniform
+        const uint32_t left = C - p.s * kSlab;
+        if (!PAL) {
+            const uint16_t* const b = static_cast<const uint16_t*>(w.w) + pos;
+            const uint32_t k0 = uint32_t(lane) * 8u, k1 = 512u + k0;
+            it.a = load_stream16(b + (k0 < left ? k0 : 0u));
+            it.b = load_stream16(b + (k1 < left ? k1 : 0u));
+            return;
+        }
+        const uint32_t k = lane16 < left ? lane16 : 0u;
+        const u32x2_t n = load_stream8(static_cast<const uint8_t*>(w.w) + pos / 2 + k / 2);
+        it.a = u32x4_t{n[0], n[1], 0u, 0u};
+        it.b = load_stream16(w.sm + pos + k);
+        const uint64_t row_tile = (pos - p.s * kSlab) >> 12;
+        const uint32_t gi = uint32_t((pos >> 6) - (row_tile << 6)), tl = p.j * tiles + (gi >> 6), gb = gi & 63u;
+        const uint64_t w0 = readlane64(word, int(tl));
+        uint64_t bits = w0 >> gb;
+        if (gb > 48u) bits |= readlane64(word, int(min(tl + 1u, p.j * tiles + tiles - 1u))) << (64u - gb);
+        const uint32_t m16 = uint32_t(bits) & 0xFFFFu;
+        const uint32_t eb = uint32_t(__builtin_amdgcn_readlane(int(ebase), int(p.j)));
+        const uint32_t start = uint32_t(__builtin_amdgcn_readlane(int(base), int(tl))) - eb +
+                               uint32_t(__popcll(gb ? w0 & ((uint64_t(1) << gb) - 1) : 0));
+        const uint32_t grp = k >> 6;
+        it.verb = (m16 >> grp) & 1u;
+        const uint32_t slot = start + uint32_t(__popc(m16 & ((1u << grp) - 1u)));
+        it.vx = load16(w.vexp + uint64_t(eb) * 64u + (it.verb ? slot * 64u + (k & 63u) : 0u));
+    };
+
+    constexpr int NS = D + 1;
+    Item<PAL> ring[NS];
+    Pos at[NS], last{0, 0};
+    if (total) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (d > 0 && uint32_t(d) < total) last = next(last);
+            at[d] = last;
+            issue(last, ring[d]);
+        }
+    }
+    const uint32_t chunks = C / 8u, all = slabs * (kSlab / 8);
+    for (uint32_t j = 0; j < chosen; ++j) {
+        const uint16_t* const x = a.X + int64_t(__builtin_amdgcn_readlane(pl, int(j))) * a.ldx;
+        for (uint32_t i = uint32_t(tid); i < all; i += 64u * kGemvWaves) {
+            const u32x4_t v = i < chunks ? load16(x + i * 8u) : u32x4_t{0u, 0u, 0u, 0u};
+            const uint32_t in = i & 127u, to = PAL ? (i & ~127u) + (in & 1u) * 64u + (in >> 1) : i;
+            store16(xs + (j * all + to) * 8u, v);
+        }
+    }
+    float residual = 0.f;
+    if (c.residual)
+        residual = c.residual_type == VT_F32 ? static_cast<const float*>(c.residual)[row]
+                                             : bf16_value(static_cast<const uint16_t*>(c.residual)[row]);
+    __syncthreads();
+
+    float acc = 0.f, sum = 0.f;
+    auto compute = [&](Pos p, const Item<PAL>& it) {
+        uint32_t v[8];
+        item_weights<PAL>(it, reinterpret_cast<const char*>(lut), v);
+        const uint32_t left = C - p.s * kSlab;
+        if (left < uint32_t(kSlab)) cut_weights<PAL>(left, lane, v);
+        acc = item_dot(v, xs + (p.j * all + p.s * 128u + uint32_t(lane)) * 8u, acc);
+        if (p.s + 1 < slabs) return;
+        sum = fmaf(__uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(wt)), int(p.j)))),
+                   wave_sum(acc), sum);
+        acc = 0.f;
+    };
+    uint32_t done = 0;
+    for (; done + NS <= total; done += NS) {
+#pragma unroll
+        for (int d = 0; d < NS; ++d) {
+            if (done + uint32_t(d) + D < total) last = next(last);
+            at[(d + D) % NS] = last;
+            issue(last, ring[(d + D) % NS]);
+            compute(at[d], ring[d]);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < NS - 1; ++d)
+        if (done + uint32_t(d) < total) compute(at[d], ring[d]);
+    if (lane == 0 && mine) {
+        if (c.residual) sum += residual;
+        if (c.out_type == VT_BF16) static_cast<uint16_t*>(c.out)[row] = uint16_t(f32_to_bf16_rne(sum));
+        else static_cast<float*>(c.out)[row] = sum;
+    }
+}
+
 // Rows of a wave: one, or two on tall matrices (a wave's start is paid for half
 // as often; single matrices only, 65536 x 4096: 65 us against 77), as long as
 // the tables of its tiles fit its lanes.
@@ -294,6 +437,18 @@ hipError_t launch_gemv_rows(bool pal, bool pair, const GroupArgs& a, int nb, hip
                    : (pair ? launch<false, true, 1>(a, s) : launch<false, false, 1>(a, s));
     return pal ? (pair ? launch<true, true, 2>(a, s) : launch<true, false, 2>(a, s))
                : (pair ? launch<false, true, 2>(a, s) : launch<false, false, 2>(a, s));
+}
+
+// A row's tiles of every chosen expert fit the lanes, the inputs 48 KB.
+bool gemv_combine_supported(const GroupArgs& a, int top_k) {
+    return top_k * ((a.C + 4095) / 4096 + 1) <= 64 && staged_bytes(a, top_k) <= 48 * 1024;
+}
+
+hipError_t launch_gemv_combine(bool pal, const GroupArgs& a, const CombineArgs& c, hipStream_t s) {
+    const dim3 grid(unsigned((a.R + kGemvWaves - 1) / kGemvWaves)), block(64 * kGemvWaves);
+    if (pal) launch_timed(gemv_combine_kernel<true, 2>, grid, block, staged_bytes(a, c.top_k), s, a, c);
+    else launch_timed(gemv_combine_kernel<false, 2>, grid, block, staged_bytes(a, c.top_k), s, a, c);
+    return hipGetLastError();
 }
 
 }  // namespace uwk

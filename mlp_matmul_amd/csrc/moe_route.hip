@@ -23,8 +23,7 @@
 // launch for the selection and the blocks' counts, and one for the places.
 #include <float.h>
 
-#include "device_common.h"
-#include "experts.h"
+#include "grouped_common.h"
 
 namespace uwk {
 
@@ -32,7 +31,7 @@ namespace {
 
 constexpr int kRT = 1024;            // threads of a workgroup
 constexpr int kRW = kRT / 64;        // its waves
-constexpr int kMaxBlocks = 128;
+constexpr int kMaxBlocks = 256;         // one a compute unit: 16384 tokens in blocks of 64
 
 template <int N>
 __device__ __forceinline__ uint32_t row_ror(uint32_t v) {
@@ -142,6 +141,7 @@ template <int PHASE>
 __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     __shared__ uint32_t cnt[kRW][kMaxExperts];             // slots of each wave, then the next place of each
     __shared__ uint32_t wave_total[kMaxExperts / 64];
+    __shared__ uint32_t part[2][PHASE == 2 ? kRT : 1];     // (before, in all) of each group of blocks
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t lane = uint32_t(tid) & 63u, sub = lane & 15u;
     const int E = a.experts, K = a.top_k;
@@ -170,19 +170,32 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     }
 
     // slots of every expert, before this block and in all; then where each
-    // expert starts: a scan over the experts
+    // expert starts: a scan over the experts.  The blocks' counts are summed by
+    // as many groups of threads as fit, 16 loads on their way at a time.
     uint32_t before = 0, total = 0;
-    if (tid < E) {
-        if (PHASE == 2) {
-            for (int b = 0; b < a.blocks; ++b) {
-                const uint32_t c = uint32_t(a.counts[int64_t(b) * E + tid]);
-                total += c;
-                if (b < int(blockIdx.x)) before += c;
+    if (PHASE == 2) {
+        const int ep = (E + 63) & ~63, groups = kRT / ep, g = tid / ep, e = tid % ep;
+        const int lo = a.blocks * g / groups, hi = a.blocks * (g + 1) / groups;
+        uint32_t bef = 0, tot = 0;
+        if (g < groups && e < E) {
+#pragma unroll 16
+            for (int b = lo; b < hi; ++b) {
+                const uint32_t c = uint32_t(a.counts[int64_t(b) * E + e]);
+                tot += c;
+                bef += b < int(blockIdx.x) ? c : 0u;
             }
-        } else {
-#pragma unroll
-            for (int w = 0; w < kRW; ++w) total += cnt[w][tid];
+            part[0][tid] = bef;
+            part[1][tid] = tot;
         }
+        __syncthreads();
+        if (tid < E)
+            for (int i = 0; i < groups; ++i) {
+                before += part[0][i * ep + tid];
+                total += part[1][i * ep + tid];
+            }
+    } else if (tid < E) {
+#pragma unroll
+        for (int w = 0; w < kRW; ++w) total += cnt[w][tid];
     }
     uint32_t incl = total;
 #pragma unroll
@@ -241,24 +254,24 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
         if (i >= int64_t(all)) a.order[i] = -1;
 }
 
-__device__ __forceinline__ float load_value(const void* p, int type, int64_t i) {
-    return type == VT_BF16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16)
-                           : static_cast<const float*>(p)[i];
-}
-
 // out[t] = sum_j weights[t][j] * Y[place[t][j]] (+ residual[t]), j ascending.
+// Memory bound: four columns a lane.
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-    const int64_t t = blockIdx.y + int64_t(blockIdx.z) * gridDim.y;
-    const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (t >= a.tokens || c >= a.cols) return;
-    float v = 0.f;
+    const int64_t quads = (a.cols + 3) / 4, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= a.tokens * quads) return;
+    const int64_t t = i / quads;
+    const int c = int(i % quads) * 4, C = int(a.cols);
+    const bool aligned = (C & 3) == 0;
+    f32x4_t v{0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < a.top_k; ++j) {
         const int32_t p = a.place[t * a.top_k + j];
-        if (p >= 0 && p < a.n) v = fmaf(a.weights[t * a.top_k + j], a.Y[int64_t(p) * a.cols + c], v);
+        if (p < 0 || p >= a.n) continue;
+        const f32x4_t y = load4(a.Y, VT_F32, int64_t(p) * C + c, c, C, aligned);
+        const float w = a.weights[t * a.top_k + j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = fmaf(w, y[k], v[k]);
     }
-    if (a.residual) v += load_value(a.residual, a.residual_type, t * a.ldr + c);
-    if (a.out_type == VT_BF16) static_cast<uint16_t*>(a.out)[t * a.ldo + c] = uint16_t(f32_to_bf16_rne(v));
-    else static_cast<float*>(a.out)[t * a.ldo + c] = v;
+    epilogue4(Epilogue{nullptr, a.residual, a.out, a.ldr, a.ldo, VT_F32, a.residual_type, a.out_type, ACT_NONE}, t, c, C, v);
 }
 
 }  // namespace
@@ -284,9 +297,9 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {
     if (a.tokens <= 0 || a.cols <= 0) return hipSuccess;
-    const unsigned y = unsigned(a.tokens < 32768 ? a.tokens : 32768);
-    const dim3 grid(unsigned((a.cols + 255) / 256), y, unsigned((a.tokens + y - 1) / y));
-    combine_kernel<<<grid, 256, 0, s>>>(a);
+    const int64_t quads = a.tokens * ((a.cols + 3) / 4), blocks = (quads + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    combine_kernel<<<unsigned(blocks), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -417,6 +417,25 @@ def test_layer(torch_cuda, tokens, experts, top_k, pal):
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("pal", [False, True])
+def test_layer_single_token(torch_cuda, pal):
+    """One token: more experts than it can have, masked ones among them, none
+    at all, rows of several tiles of 64 groups and of parts of one."""
+    torch = torch_cuda
+    for experts, top_k, F, H in ((8, 8, 64, 64), (5, 3, 1088, 320), (20, 16, 192, 128), (3, 2, 8256, 64), (6, 4, 64, 4160)):
+        print_case(f"layer of one token, {experts} experts, top {top_k}, F={F} H={H} pal={pal}")
+        (G, g), (U, u), (D, d) = (make_weight(torch, 80 + i, experts, r, c, pal, 0.01) for i, (r, c) in
+                                  enumerate(((F, H), (F, H), (H, F))))
+        X = rows_of(torch, 6, 1, H)
+        for masked in (0, 2, experts):
+            logits = torch.randn(1, experts, generator=torch.Generator().manual_seed(masked)).cuda()
+            logits[0, :masked] = -math.inf
+            for res, out_dtype in ((None, torch.float32), (X, torch.bfloat16), (X.float(), torch.float32)):
+                y, err = layer_reference(torch, g, u, d, f64(X), logits, top_k, True, res)
+                out = uw.moe_layer(G, U, D, X, logits, top_k, residual=res, out_dtype=out_dtype)
+                check(torch, out, y, err, f"layer of one token, masked {masked}")
+
+
 def test_block_together(torch_cuda):
     """Router projection with its bias, routing, the layer added to the
     residual stream in place, then a projection on it, as a model would."""
