@@ -427,10 +427,11 @@ enum {                                             /* activations, in fp32 */
 /* out[b][r] = act(sum_c X[b][c] W[r][c] + bias[r]) + residual[b][r].
  * bias [rows] and residual [batch, rows] may be NULL; out may be the residual
  * itself (same pointer, stride and type), and overlaps nothing else.
- * scratch: NULL, or uw_linear_scratch_bytes() bytes, which compressed weights
- * use above 32 rows (sums of K-slices, or the matrix as bf16); with less than
- * that the weights are rebuilt tile by tile, slower.  Calls that share it must
- * be ordered.  Results with and without it agree to rounding. */
+ * scratch: NULL, or uw_linear_scratch_bytes() bytes (0 through 16 rows) for
+ * sums of K-slices, where they fill the chip, and for large batches of
+ * compressed weights the matrix as bf16; with less than that K is not split and
+ * the weights are rebuilt tile by tile, slower.  Calls that share it must be
+ * ordered.  Results with and without it agree to rounding. */
 int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols,
               const uint16_t* X, int64_t ldx, int64_t batch,
               const void* bias, int bias_type, int act,

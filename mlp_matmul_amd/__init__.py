@@ -471,8 +471,8 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
         raise ValueError(f"bias must be a contiguous [{rows}] tensor")
     res, res_type, ldr = _residual_arg(residual, batch, rows)
     out, ldo, out_type = _out_arg(out, batch, rows, out_dtype, dev)
-    if scratch is None and d is not None and batch > 32:
-        need = lib().uw_linear_scratch_bytes(1, rows, cols, batch)
+    if scratch is None and batch > 16:                       # never any through 16 rows
+        need = lib().uw_linear_scratch_bytes(0 if d is None else 1, rows, cols, batch)
         if need > 0:
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
     sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())

@@ -126,6 +126,7 @@ uwk::GroupArgs group_args(const uint16_t* X, int64_t x_rows, int64_t ldx, const 
     a.R = int32_t(rows);
     a.C = int32_t(cols);
     a.div = top_k;
+    a.split = 1;
     a.cus = uw::device_cus();
     return a;
 }

@@ -43,6 +43,8 @@ struct GroupArgs {
     int32_t E, R, C, div;
     Epilogue ep;                // the pair: only out (bf16) and ldo
     int32_t cus;
+    int32_t split;              // K-slices of the bf16 tile kernel without offsets (1: none)
+    float* sums;                // [split, n, R] of them when split > 1: out is not written
 };
 
 struct CombineArgs {

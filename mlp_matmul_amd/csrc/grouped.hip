@@ -16,40 +16,58 @@ namespace uwk {
 
 namespace {
 
-// A tile shape's time for one 64-column step of its workgroups, in us on
-// MI355X: `full` with every compute unit taken (8192 x 8192 x 8192: 2424, 1362,
-// 984, 916 us), `one` with a workgroup here and there (64 rows of 14336 x 4096:
-// 23.5, 26.7, 47.7, 79 us, less 4 us for launch and epilogue).
+// A tile shape's time for one 64-column step of a round of workgroups, in us on
+// MI355X: with a workgroup here and there, with one on each compute unit, and
+// with `per_cu` on each.
 struct TileCost {
     int mt, nt, per_cu;
-    double full, one;
+    double few, one, full;
 };
-constexpr TileCost kTiles[TILE_SHAPES] = {
-    {64, 64, 2, 0.59, 0.30}, {128, 64, 2, 0.665, 0.35}, {256, 128, 1, 0.96, 0.68}, {256, 256, 1, 1.79, 1.2}};
+constexpr TileCost kTiles[TILE_SHAPES] = {{64, 64, 2, 0.16, 0.265, 0.51},
+                                          {128, 64, 2, 0.34, 0.45, 0.86},
+                                          {256, 128, 1, 0.65, 0.96, 0.96},
+                                          {256, 256, 1, 1.2, 1.7, 1.7}};
+// A launch with its first loads and its stores, bytes a us from memory and the
+// share of them that a second reading of the weights or the rows costs, and the
+// kernel that adds slices, with the bytes a us of writing and reading them.
+constexpr double kLaunchUs = 6, kBytesUs = 7.8e6, kWeightsAgain = 0.45, kRowsAgain = 0.33, kSumsUs = 2, kSumsBytesUs = 3.9e6;
 
-// Time of `groups` products of `rows` input rows each with [R, C]: the rounds
-// of workgroups that the chip takes, the last one by how full it is.
-double tile_us(const TileCost& c, bool pair, double groups, double rows, bool exact, const GroupArgs& a) {
-    const int mt = pair ? c.mt / 2 : c.mt;
-    // tiles of an expert: the rows are spread, half a tile is lost on average
-    const double tiles = exact ? double((int64_t(rows) + c.nt - 1) / c.nt) : std::max(1.0, rows / c.nt + 0.5);
-    const double units = groups * tiles * double((a.R + mt - 1) / mt), slots = double(a.cus) * c.per_cu;
-    const double rounds = double(int64_t(units / slots)), rest = units / slots - rounds;
-    return (rounds * c.full + (rest > 0 ? c.one + (c.full - c.one) * rest : 0)) * double(a.C / 64) + 4;
-}
+struct TilePlan {
+    TileShape shape;
+    int split;
+    double us;
+};
 
-TileShape best_tile(bool pair, double groups, double rows, bool exact, const GroupArgs& a, double* us = nullptr) {
-    int best = 0;
-    double t = 1e30;
+// The tile shape and number of K-slices for `groups` products of `rows` input
+// rows each with [R, C]: the choice of the least estimated time, which is the
+// rounds of workgroups that the chip takes or the bytes from memory, whichever
+// is longer.  The constants are fitted to the 16 choices at 32 sizes (1000 x
+// 2048 to 14336 x 4096 and 4096 x 14336, 33 to 2049 rows); what it picks there is
+// the fastest choice or within 8% of it.  At 4096 x 14336, us, against 64 x 64
+// tiles without slices: 64 rows 31 (128 x 64, 8 slices) and 73, 256 rows 48
+// (256 x 128, 8) and 72, 800 rows 106 (256 x 128, 2) and 198.
+TilePlan plan_tiles(bool pair, double groups, double rows, bool exact, bool may_split, const GroupArgs& a) {
+    TilePlan best{TILE_64x64, 1, 1e30};
+    const double weights = groups * double(a.R) * double(a.C) * (pair ? 4 : 2);
     for (int i = 0; i < TILE_SHAPES; ++i) {
-        const double v = tile_us(kTiles[i], pair, groups, rows, exact, a);
-        if (v < t) {
-            t = v;
-            best = i;
+        const TileCost& c = kTiles[i];
+        const int mt = pair ? c.mt / 2 : c.mt;
+        const double bands = groups * double((a.R + mt - 1) / mt);
+        // tiles of an expert: the rows are spread, half a tile is lost on average
+        const double tiles = exact ? double((int64_t(rows) + c.nt - 1) / c.nt) : std::max(1.0, rows / c.nt + 0.5);
+        const double again = kWeightsAgain * weights * (tiles - 1) + kRowsAgain * bands * rows * double(a.C) * 2;
+        for (int split = 1; split <= (may_split ? 8 : 1) && split * 2 <= std::max(2, a.C / 64); split *= 2) {
+            const double per = bands * tiles * split / a.cus;          // workgroups a compute unit
+            const double rounds = double(int64_t(per / c.per_cu)), rest = per - rounds * c.per_cu;
+            double round = rounds * c.full;
+            if (rest > 1) round += c.one + (c.full - c.one) * (rest - 1);
+            else if (rest > 0) round += c.few + (c.one - c.few) * rest;
+            double us = kLaunchUs + std::max(round * double(a.C / 64) / split, (weights + again) / kBytesUs);
+            if (split > 1) us += kSumsUs + split * rows * double(a.R) * 8 / kSumsBytesUs;
+            if (us < best.us) best = {TileShape(i), split, us};
         }
     }
-    if (us) *us = t;
-    return TileShape(best);
+    return best;
 }
 
 // ------------------------------------------------------------ direct palette to bf16
@@ -126,25 +144,30 @@ PalPlan pal_plan(const GroupArgs& a) {
                                                                                                  : PLAN_TILES;
 }
 
-uint64_t plan_bytes(PalPlan p, const GroupArgs& a, int* split = nullptr) {
-    if (p == PLAN_TILES) return 0;
-    if (p == PLAN_EXPAND) return uint64_t(a.R) * uint64_t(a.C) * 2;
-    const int k = mfma_default_split(SRC_PAL, mat_args(a), a.cus);
-    if (split) *split = k;
-    return uint64_t(k) * uint64_t(a.n) * uint64_t(a.R) * 4;
+// Whether n rows are left to the skinny kernel: through 16, and through 32 on
+// matrices below 2^25 weights (24 rows of 4096 x 4096: 10 us against 13; of
+// 14336 x 4096: 34 against 29, palette 40 against 33).
+bool few_rows(const GroupArgs& a) { return a.n <= 16 || (a.n <= 32 && int64_t(a.R) * a.C < (int64_t(1) << 25)); }
+
+uint64_t sums_bytes(const GroupArgs& a, int split) { return uint64_t(split) * uint64_t(a.n) * uint64_t(a.R) * 4; }
+
+hipError_t add_sums(const GroupArgs& a, const float* sums, int split, hipStream_t s) {
+    const int64_t quads = a.n * ((a.R + 3) / 4);
+    sums_epilogue_kernel<<<unsigned((quads + 255) / 256), 256, 0, s>>>(sums, split, a.n, a.R, a.ep);
+    return hipGetLastError();
 }
 
-// bf16 rows above the skinny kernel's; a few rows behind the last whole tile go
-// to the skinny kernel where they would start another round of tiles (2049
-// rows of 4096 x 4096: 61 + 9 us against 100).
-hipError_t linear_tiles(const GroupArgs& a, hipStream_t s) {
-    double whole_us = 0, us = 0;
-    const TileShape shape = best_tile(false, 1, double(a.n), true, a, &us);
+// bf16 tiles.  A few rows behind the last whole tile go to the skinny kernel
+// where they would start another round of tiles (2049 rows of 4096 x 4096: 61 +
+// 9 us against 95).
+hipError_t linear_tiles(const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s) {
+    TilePlan plan = plan_tiles(false, 1, double(a.n), true, true, a);
+    if (plan.split > 1 && sums_bytes(a, plan.split) > scratch_bytes) plan = plan_tiles(false, 1, double(a.n), true, false, a);
     const int64_t tail = a.n % 128;                      // 128 and 256 both divide what is left
     if (tail && tail <= 32 && a.n > 256) {
-        const TileShape part = best_tile(false, 1, double(a.n - tail), true, a, &whole_us);
-        // the weights once more, at 5 TB/s, and a launch
-        if (whole_us + 4 + double(a.R) * double(a.C) * 2 / 5e6 < us) {
+        const TilePlan part = plan_tiles(false, 1, double(a.n - tail), true, false, a);
+        // the weights once more, and a launch
+        if (part.us + kLaunchUs + double(a.R) * double(a.C) * 2 / kBytesUs < plan.us) {
             GroupArgs head = a, rest = a;
             head.n = head.x_rows = a.n - tail;
             rest.n = rest.x_rows = tail;
@@ -152,34 +175,44 @@ hipError_t linear_tiles(const GroupArgs& a, hipStream_t s) {
             const int64_t ob = a.ep.out_type == VT_BF16 ? 2 : 4, rb = a.ep.residual_type == VT_BF16 ? 2 : 4;
             rest.ep.out = static_cast<uint8_t*>(a.ep.out) + head.n * a.ep.ldo * ob;
             if (a.ep.residual) rest.ep.residual = static_cast<const uint8_t*>(a.ep.residual) + head.n * a.ep.ldr * rb;
-            const hipError_t e = launch_tile(false, head, part, s);
-            return e == hipSuccess ? launch_linear(false, rest, nullptr, 0, s) : e;
+            const hipError_t e = launch_tile(false, head, part.shape, s);
+            if (e != hipSuccess) return e;
+            if (tail <= 2 && gemv_rows_supported(rest, int(tail))) return launch_gemv_rows(false, false, rest, int(tail), s);
+            return launch_skinny_rows(false, false, rest, int(tail), s);
         }
     }
-    return launch_tile(false, a, shape, s);
+    GroupArgs b = a;
+    b.split = plan.split;
+    b.sums = static_cast<float*>(scratch);
+    const hipError_t e = launch_tile(false, b, plan.shape, s);
+    return e != hipSuccess || plan.split == 1 ? e : add_sums(a, b.sums, plan.split, s);
 }
+
+uint64_t expanded_bytes(const GroupArgs& a) { return (uint64_t(a.R) * uint64_t(a.C) * 2 + 255) & ~uint64_t(255); }
 
 }  // namespace
 
 uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int cus) {
-    if (!pal || batch <= 32 || rows == 0) return 0;
     GroupArgs a{};
     a.R = int32_t(rows);
     a.C = int32_t(cols);
     a.n = batch;
     a.cus = cus;
-    return plan_bytes(pal_plan(a), a);
+    if (rows == 0 || few_rows(a)) return 0;
+    const PalPlan p = pal ? pal_plan(a) : PLAN_TILES;
+    if (p == PLAN_SUMS) return sums_bytes(a, mfma_default_split(SRC_PAL, mat_args(a), cus));
+    if (pal && p == PLAN_TILES) return 0;
+    const TilePlan t = plan_tiles(false, 1, double(a.n), true, true, a);
+    return (p == PLAN_EXPAND ? expanded_bytes(a) : 0) + (t.split > 1 ? sums_bytes(a, t.split) : 0);
 }
 
 hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s) {
     if (a.n <= 0 || a.R <= 0) return hipSuccess;
     if (a.n <= 2 && gemv_rows_supported(a, int(a.n))) return launch_gemv_rows(pal, false, a, int(a.n), s);
-    if (a.n <= 32) return launch_skinny_rows(pal, false, a, int(a.n), s);
-    if (!pal) return linear_tiles(a, s);
-    PalPlan plan = pal_plan(a);
-    int split = 1;
-    if (plan_bytes(plan, a, &split) > scratch_bytes || (plan == PLAN_SUMS && a.ldx != a.C)) plan = PLAN_TILES;
-    if (plan == PLAN_EXPAND) {
+    if (few_rows(a)) return launch_skinny_rows(pal, false, a, int(a.n), s);
+    if (!pal) return linear_tiles(a, scratch, scratch_bytes, s);
+    const PalPlan plan = pal_plan(a);
+    if (plan == PLAN_EXPAND && scratch_bytes >= expanded_bytes(a)) {
         const int64_t n = int64_t(a.R) * a.C;
         uint16_t* const w = static_cast<uint16_t*>(scratch);
         expand_kernel<<<unsigned((n / 16 + 255) / 256), 256, 0, s>>>(a.w[0], n, w);
@@ -188,17 +221,16 @@ hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t s
         GroupArgs b = a;
         b.w[0] = Weight{};
         b.w[0].w = w;
-        return linear_tiles(b, s);
+        return linear_tiles(b, static_cast<uint8_t*>(scratch) + expanded_bytes(a), scratch_bytes - expanded_bytes(a), s);
     }
-    if (plan == PLAN_SUMS) {
+    if (plan == PLAN_SUMS && a.ldx == a.C) {
         MatArgs m = mat_args(a);
-        m.split_k = split;
-        m.Y = m.partial = static_cast<float*>(scratch);
-        const hipError_t e = launch_mfma_sums(SRC_PAL, m, s);
-        if (e != hipSuccess) return e;
-        const int64_t quads = a.n * ((a.R + 3) / 4);
-        sums_epilogue_kernel<<<unsigned((quads + 255) / 256), 256, 0, s>>>(m.partial, split, a.n, a.R, a.ep);
-        return hipGetLastError();
+        m.split_k = mfma_default_split(SRC_PAL, m, a.cus);
+        if (sums_bytes(a, m.split_k) <= scratch_bytes) {
+            m.Y = m.partial = static_cast<float*>(scratch);
+            const hipError_t e = launch_mfma_sums(SRC_PAL, m, s);
+            return e == hipSuccess ? add_sums(a, m.partial, m.split_k, s) : e;
+        }
     }
     // 64 x 64 tiles until they take four rounds (14336 x 4096, 64 rows: 45 us
     // against 68), then 128 x 128 (8192 x 8192 x 8192: 1.60 against 2.9 ms)
@@ -221,7 +253,7 @@ hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s
     // 12 rows of 32 experts: 16-row ones 62 (bf16), 72 us (palette, 63 with tiles)
     if (rows <= (pal ? 1.5 : 2.5)) return launch_skinny_rows(pal, pair, a, 4, s);
     if (rows <= (pal ? 11 : 14)) return launch_skinny_rows(pal, pair, a, 16, s);
-    if (!pal) return launch_tile(pair, a, best_tile(pair, double(groups), rows, false, a), s);
+    if (!pal) return launch_tile(pair, a, plan_tiles(pair, double(groups), rows, false, false, a).shape, s);
     // 25 rows of 8 experts: 128 x 64 tiles 111 us, 128 x 128 123; 64 rows: 151
     // and 122
     return launch_tile_pal(pair, a, rows <= 40 ? PAL_TILE_128x64 : PAL_TILE_128x128, s);

@@ -9,7 +9,7 @@ namespace uwk {
 
 // Rows [row0, row0 + rows) of expert e against weight rows of band `band`.
 struct GroupTile {
-    int32_t e, rows, band;
+    int32_t e, rows, band, slice;    // slice: of K, with a.split
     int64_t row0;
 };
 
@@ -54,6 +54,7 @@ __device__ __forceinline__ bool group_tile_of(const GroupArgs& a, uint32_t bands
     const uint32_t u = spread_unit(uint32_t(min(units, uint64_t(gridDim.x))), blockIdx.x);
     const uint32_t tile = u / bands;                       // never past the last: u < total * bands
     bool found = false;
+    t.slice = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const uint64_t past = __builtin_amdgcn_ballot_w64(end[c] > tile);
@@ -83,11 +84,12 @@ __device__ __forceinline__ bool group_tile_of(const GroupArgs& a, uint32_t bands
 template <int NT>
 __device__ __forceinline__ bool group_tile(const GroupArgs& a, uint32_t bands, GroupTile& t) {
     if (!a.offsets) {
-        const uint32_t tiles = uint32_t((a.n + NT - 1) / NT), total = tiles * bands;
+        const uint32_t tiles = uint32_t((a.n + NT - 1) / NT), total = tiles * bands * uint32_t(a.split);
         if (blockIdx.x >= total) return false;
         const uint32_t u = spread_unit(total, blockIdx.x);
         t.e = 0;
-        t.band = int32_t(u / tiles);
+        t.slice = int32_t(u / (tiles * bands));
+        t.band = int32_t(u / tiles % bands);
         t.row0 = int64_t(u % tiles) * NT;
         t.rows = int32_t(min(int64_t(NT), a.n - t.row0));
         return true;
@@ -97,7 +99,7 @@ __device__ __forceinline__ bool group_tile(const GroupArgs& a, uint32_t bands, G
 
 // Most units a grid needs: every expert with rows has at most n_e/NT + 1 tiles.
 inline int64_t group_units(const GroupArgs& a, int nt, int64_t bands) {
-    if (!a.offsets) return (a.n + nt - 1) / nt * bands;
+    if (!a.offsets) return (a.n + nt - 1) / nt * bands * a.split;
     return (a.n / nt + (a.n < a.E ? a.n : a.E)) * bands;
 }
 

@@ -58,7 +58,10 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t lane = uint32_t(tid) & 63u, q = lane >> 4, rl = lane & 15u;
     const uint32_t R = uint32_t(a.R), C = uint32_t(a.C);
-    const uint32_t row0 = uint32_t(t.band) * kRows, steps = C / kStep;
+    const uint32_t row0 = uint32_t(t.band) * kRows;
+    // the slice's steps (all of them without a split)
+    const uint32_t s_lo = uint32_t(uint64_t(C / kStep) * uint32_t(t.slice) / uint32_t(a.split));
+    const uint32_t steps = uint32_t(uint64_t(C / kStep) * uint32_t(t.slice + 1) / uint32_t(a.split)) - s_lo;
     const int64_t first = int64_t(t.e) * R * C;
 
     // sources: load j of this wave covers 8 rows of the tile
@@ -85,7 +88,7 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
     // steps past the end load the last one again: the waits count the same loads in every step
     auto load = [&](uint32_t s, int i) {
         uint16_t* const w = buffer(i), * const x = w + MT * kStep;
-        s = min(s, steps - 1u);
+        s = s_lo + min(s, steps - 1u);
 #pragma unroll
         for (int j = 0; j < WD; ++j) {
             const int m = PAIR ? (wave * WD + j) * 8 / kRows : 0;          // uniform
@@ -174,6 +177,9 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
     // 4*(l/16)..+3 of a block.
     constexpr int OM = PAIR ? FM / 2 : FM;
     float* const part = reinterpret_cast<float*>(buf0);
+    Epilogue ep = a.ep;
+    if (!PAIR && a.split > 1)
+        ep = Epilogue{nullptr, nullptr, a.sums + int64_t(t.slice) * a.n * a.R, 0, a.R, VT_F32, VT_F32, VT_F32, ACT_NONE};
 #pragma unroll 1
     for (int p = 0; p < FN; ++p) {
         __syncthreads();
@@ -196,7 +202,7 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
             const int n = i / (kRows / 4), r = i % (kRows / 4) * 4;
             const int b = ((n / 16) * FN + p) * 16 + n % 16;               // input row of the tile
             if (b < t.rows && row0 + uint32_t(r) < R)
-                epilogue4(a.ep, t.row0 + b, int(row0) + r, a.R, *reinterpret_cast<const f32x4_t*>(part + n * ES + r));
+                epilogue4(ep, t.row0 + b, int(row0) + r, a.R, *reinterpret_cast<const f32x4_t*>(part + n * ES + r));
         }
     }
 }

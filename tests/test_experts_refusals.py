@@ -143,8 +143,11 @@ def test_scratch_sizes():
     assert L.uw_linear_scratch_bytes(1, 64, 100, 4) == _capi.UW_EINVAL
     assert L.uw_linear_scratch_bytes(1, 1 << 20, 1 << 11, 4) == _capi.UW_EUNSUPPORTED
     assert L.uw_linear_scratch_bytes(1, 4096, 4096, 32) == 0
-    assert L.uw_linear_scratch_bytes(0, 4096, 4096, 5000) == 0
-    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 5000) == 2 * 4096 * 4096
+    assert L.uw_linear_scratch_bytes(0, 4096, 4096, 16) == 0
+    assert L.uw_linear_scratch_bytes(0, 8192, 8192, 8192) == 0
+    assert L.uw_linear_scratch_bytes(1, 8192, 8192, 8192) == 2 * 8192 * 8192
+    assert L.uw_linear_scratch_bytes(0, 4096, 14336, 64) % (64 * 4096 * 4) == 0
+    assert L.uw_linear_scratch_bytes(0, 4096, 14336, 64) > 0
     assert L.uw_linear_scratch_bytes(1, 4096, 4096, 100) % (100 * 4096 * 4) == 0
 
 
