@@ -135,7 +135,7 @@ uwk::GroupArgs group_args(const uint16_t* X, int64_t x_rows, int64_t ldx, const 
 uint64_t route_scratch(int64_t tokens, int64_t experts) {
     int32_t blocks, per;
     uwk::route_blocks(tokens, &blocks, &per);
-    return blocks > 1 ? align256(uint64_t(blocks) * uint64_t(experts) * 4) : 0;
+    return blocks > 1 ? align256(uint64_t(blocks) * uint64_t((experts + 7) / 8) * 16) : 0;
 }
 
 int check_routing(int64_t tokens, int experts, int top_k, const char* who) {
@@ -242,7 +242,7 @@ int uw_moe_route(const void* logits, int logits_type, int64_t ld, int64_t tokens
         if (need && (!scratch || !aligned16(scratch) || scratch_bytes < need))
             return bad(who, "scratch smaller than uw_moe_route_scratch_bytes()");
         uwk::RouteArgs a{logits, ld,  tokens,  logits_type, experts, top_k, renormalize != 0, ids, weights,
-                         offsets, order, place, static_cast<int32_t*>(scratch), 0, 0};
+                         offsets, order, place, static_cast<uint16_t*>(scratch), 0, 0};
         uwk::route_blocks(tokens, &a.blocks, &a.per_block);
         const hipError_t e = uwk::launch_route(a, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);

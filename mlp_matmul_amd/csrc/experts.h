@@ -91,7 +91,7 @@ struct RouteArgs {
     int32_t* offsets;
     int32_t* order;
     int32_t* place;
-    int32_t* counts;            // [blocks, experts] of every block's slots, when blocks > 1
+    uint16_t* counts;           // [blocks, experts up to 8s] of every block's slots, when blocks > 1
     int32_t blocks, per_block;  // tokens of a block: a multiple of 64
 };
 

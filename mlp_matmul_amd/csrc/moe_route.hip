@@ -23,6 +23,8 @@
 // launch for the selection and the blocks' counts, and one for the places.
 #include <float.h>
 
+#include <algorithm>
+
 #include "grouped_common.h"
 
 namespace uwk {
@@ -31,7 +33,7 @@ namespace {
 
 constexpr int kRT = 1024;            // threads of a workgroup
 constexpr int kRW = kRT / 64;        // its waves
-constexpr int kMaxBlocks = 256;         // one a compute unit: 16384 tokens in blocks of 64
+constexpr int kMaxBlocks = 256;      // one a compute unit (16384 tokens in blocks of 64), until 16 bits end
 
 template <int N>
 __device__ __forceinline__ uint32_t row_ror(uint32_t v) {
@@ -67,132 +69,182 @@ __device__ __forceinline__ float order_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-__device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t t, int e) {
-    const int64_t i = t * a.ld + e;
-    return a.type == VT_BF16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(a.logits)[i]) << 16)
-                             : static_cast<const float*>(a.logits)[i];
-}
-
 // Selects the experts of tokens t (one per DPP row; t >= tokens: nothing) and
-// counts them in cnt[expert].  V logits a lane: expert 16*c + lane.
+// counts them in cnt[expert].  V logits a lane, in runs of four where V allows
+// a wide load.
 template <int V>
 __device__ void select(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt) {
+    constexpr int W = V < 4 ? 1 : 4;
     const bool live = t < a.tokens;
+    auto expert = [&](int c) { return uint32_t(16 * W * (c / W) + c % W) + W * sub; };
     uint32_t key[V];
+    // every load stays inside the logits and none waits for another
+    float f[V];
+    const int E = a.experts;
+    const int64_t row = min(t, a.tokens - 1) * a.ld;
+    const float* const pf = static_cast<const float*>(a.logits) + row;
+    const uint16_t* const ph = static_cast<const uint16_t*>(a.logits) + row;
+    if (W == 4 && ((a.ld | E) & 3) == 0 && (reinterpret_cast<uint64_t>(a.logits) & 15) == 0) {
+        if (a.type == VT_F32) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        const int e = 16 * c + int(sub);
-        key[c] = 0;                                        // no such expert, -inf, NaN
-        if (live && e < a.experts) {
-            const float f = load_logit(a, t, e);
-            if (f > -INFINITY) key[c] = order_key(fminf(f, FLT_MAX));
+            for (int c = 0; c + W <= V; c += W) {
+                const f32x4_t q = *reinterpret_cast<const f32x4_t*>(pf + min(int(expert(c)), E - W));
+#pragma unroll
+                for (int k = 0; k < W; ++k) f[c + k] = q[k];
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c + W <= V; c += W) {
+                const u32x2_t q = *reinterpret_cast<const u32x2_t*>(ph + min(int(expert(c)), E - W));
+#pragma unroll
+                for (int k = 0; k < W; ++k) f[c + k] = __uint_as_float(k & 1 ? q[k / 2] & 0xFFFF0000u : q[k / 2] << 16);
+            }
         }
+    } else if (a.type == VT_F32) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) f[c] = pf[min(int(expert(c)), E - 1)];
+    } else {
+#pragma unroll
+        for (int c = 0; c < V; ++c) f[c] = bf16_value(ph[min(int(expert(c)), E - 1)]);
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+        key[c] = live && int(expert(c)) < E && f[c] > -INFINITY ? order_key(fminf(f[c], FLT_MAX)) : 0;
+    auto largest = [&]() {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int c = 1; c < V; ++c) m = max(m, key[c]);
+        return row_max(m);
+    };
+    float sum = 0.f;
+    if (!a.renorm) {
+        const float top = order_value(largest());
+#pragma unroll
+        for (int c = 0; c < V; ++c) sum += key[c] ? expf(order_value(key[c]) - top) : 0.f;
+        sum = row_sum(sum);
     }
     uint32_t my_key = 0, my_id = ~0u, top = 0;
-    float all = 0.f, chosen = 0.f;
     for (int j = 0; j < a.top_k; ++j) {
-        uint32_t best = 0, at = ~0u;
+        const uint32_t m = largest(), find = max(m, 1u);   // 1 is a NaN's key: with m = 0 nothing is found
+        bool has[V];
+        uint32_t at = ~0u;
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-            if (key[c] > best) {
-                best = key[c];
-                at = 16u * c + sub;
-            }
-        const uint32_t m = row_max(best);
-        const uint32_t e = row_min(best == m && m ? at : ~0u);
-        if (j == 0) {
-            top = m;
-            if (!a.renorm) {
-#pragma unroll
-                for (int c = 0; c < V; ++c) all += key[c] ? expf(order_value(key[c]) - order_value(m)) : 0.f;
-                all = row_sum(all);
-            }
+        for (int c = V - 1; c >= 0; --c) {
+            has[c] = key[c] == find;
+            at = has[c] ? expert(c) : at;
         }
+        const uint32_t e = row_min(at);
+        bool open = m && at == e;                          // this lane has it: its lowest one goes
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-            if (e == 16u * c + sub) key[c] = 0;
-        if (m) chosen += expf(order_value(m) - order_value(top));
+        for (int c = 0; c < V; ++c) {
+            key[c] = has[c] && open ? 0 : key[c];
+            open = open && !has[c];
+        }
+        top = j == 0 ? m : top;
         if (uint32_t(j) == sub) {
             my_key = m;
             my_id = e;
         }
     }
+    float w = my_key ? expf(order_value(my_key) - order_value(top)) : 0.f;
+    if (a.renorm) sum = row_sum(w);
     if (live && int(sub) < a.top_k) {
         const int64_t o = t * a.top_k + sub;
-        const float w = my_key ? expf(order_value(my_key) - order_value(top)) / (a.renorm ? chosen : all) : 0.f;
         a.ids[o] = int32_t(my_id);
-        a.weights[o] = w;
+        a.weights[o] = my_key ? w / sum : 0.f;
         if (my_key) atomicAdd(cnt + my_id, 1u);
     }
 }
 
-__device__ __forceinline__ void select_any(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt) {
-    if (a.experts <= 16) select<1>(a, t, sub, cnt);
-    else if (a.experts <= 32) select<2>(a, t, sub, cnt);
-    else if (a.experts <= 64) select<4>(a, t, sub, cnt);
-    else if (a.experts <= 128) select<8>(a, t, sub, cnt);
-    else if (a.experts <= 256) select<16>(a, t, sub, cnt);
-    else select<32>(a, t, sub, cnt);
-}
-
 // PHASE 0: everything (one block); 1: selection and the block's counts; 2:
-// offsets and places.
-template <int PHASE>
+// offsets and places.  Every block of phase 2 adds up the counts of all: 16
+// bits each, so that 16-byte loads bring eight experts' and all of a thread's
+// loads are on their way at once, from the kernel's first instruction on.
+// V: logits a lane.
+template <int PHASE, int V>
 __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
-    __shared__ uint32_t cnt[kRW][kMaxExperts];             // slots of each wave, then the next place of each
+    __shared__ uint32_t cnt[PHASE == 1 ? 1 : kRW][kMaxExperts];     // slots of each wave, then the next place of each
     __shared__ uint32_t wave_total[kMaxExperts / 64];
-    __shared__ uint32_t part[2][PHASE == 2 ? kRT : 1];     // (before, in all) of each group of blocks
+    __shared__ __align__(16) uint32_t part[2][PHASE == 2 ? kRT * 8 : 1];   // (before, in all) of each group of blocks
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t lane = uint32_t(tid) & 63u, sub = lane & 15u;
-    const int E = a.experts, K = a.top_k;
+    const int E = a.experts, K = a.top_k, vecs = (E + 7) / 8;
     const int64_t tb = int64_t(blockIdx.x) * a.per_block;  // the block's tokens, the wave's inside them
     const int64_t t_lo = tb + int64_t(wave) * (a.per_block / kRW), t_hi = min(t_lo + a.per_block / kRW, a.tokens);
-    for (int i = tid; i < kRW * E; i += kRT) cnt[i / E][i % E] = 0;
+    auto slot_id = [&](int64_t i) { return i < t_hi * K ? a.ids[i] : -1; };
+
+    const int groups = min(kRT / vecs, 32), g = tid / vecs;                // of blocks; this thread's
+    const int lo = int(int64_t(a.blocks) * g / groups), hi = g < groups ? int(int64_t(a.blocks) * (g + 1) / groups) : 0;
+    const u32x4_t* const counts = reinterpret_cast<const u32x4_t*>(a.counts) + tid % vecs;
+    constexpr int kFly = 8;
+    u32x4_t q[kFly];
+    int32_t id = -1;
+    if (PHASE == 2) {
+        id = slot_id(t_lo * K + lane);
+#pragma unroll
+        for (int i = 0; i < kFly; ++i)
+            if (lo + i < hi) q[i] = counts[int64_t(lo + i) * vecs];
+    }
+    if (PHASE == 1) {
+        for (int e = tid; e < vecs * 8; e += kRT) cnt[0][e] = 0;
+    } else {
+        for (int e = int(lane); e < E; e += 64) cnt[wave][e] = 0;
+    }
     __syncthreads();
     if (PHASE != 2) {
         for (int64_t t = t_lo; t < t_hi; t += 4) {
             const int64_t mine = t + (lane >> 4);
-            select_any(a, mine < t_hi ? mine : a.tokens, sub, cnt[wave]);
+            select<V>(a, mine < t_hi ? mine : a.tokens, sub, cnt[PHASE == 1 ? 0 : wave]);
         }
     } else {
-        for (int64_t i = t_lo * K + lane; i < t_hi * K; i += 64)
+        if (id >= 0) atomicAdd(&cnt[wave][id], 1u);
+        for (int64_t i = t_lo * K + 64 + lane; i < t_hi * K; i += 64)
             if (a.ids[i] >= 0) atomicAdd(&cnt[wave][a.ids[i]], 1u);
+        uint32_t bef[8] = {}, tot[8] = {};
+        for (int b = lo; b < hi; b += kFly) {
+#pragma unroll
+            for (int i = 0; i < kFly; ++i) {
+                if (b + i >= hi) continue;
+                const bool before = b + i < int(blockIdx.x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t l = q[i][k] & 0xFFFFu, h = q[i][k] >> 16;
+                    tot[2 * k] += l;
+                    tot[2 * k + 1] += h;
+                    bef[2 * k] += before ? l : 0u;
+                    bef[2 * k + 1] += before ? h : 0u;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kFly; ++i)
+                if (b + kFly + i < hi) q[i] = counts[int64_t(b + kFly + i) * vecs];
+        }
+        if (g < groups) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                *reinterpret_cast<u32x4_t*>(&part[0][tid * 8 + k]) = u32x4_t{bef[k], bef[k + 1], bef[k + 2], bef[k + 3]};
+                *reinterpret_cast<u32x4_t*>(&part[1][tid * 8 + k]) = u32x4_t{tot[k], tot[k + 1], tot[k + 2], tot[k + 3]};
+            }
+        }
     }
     __syncthreads();
     if (PHASE == 1) {
-        if (tid < E) {
-            uint32_t s = 0;
-#pragma unroll
-            for (int w = 0; w < kRW; ++w) s += cnt[w][tid];
-            a.counts[int64_t(blockIdx.x) * E + tid] = int32_t(s);
-        }
+        uint32_t* const out = reinterpret_cast<uint32_t*>(a.counts) + int64_t(blockIdx.x) * vecs * 4;
+        if (tid < vecs * 4) out[tid] = cnt[0][2 * tid] | (cnt[0][2 * tid + 1] << 16);
         return;
     }
 
     // slots of every expert, before this block and in all; then where each
-    // expert starts: a scan over the experts.  The blocks' counts are summed by
-    // as many groups of threads as fit, 16 loads on their way at a time.
+    // expert starts: a scan over the experts
     uint32_t before = 0, total = 0;
     if (PHASE == 2) {
-        const int ep = (E + 63) & ~63, groups = kRT / ep, g = tid / ep, e = tid % ep;
-        const int lo = a.blocks * g / groups, hi = a.blocks * (g + 1) / groups;
-        uint32_t bef = 0, tot = 0;
-        if (g < groups && e < E) {
-#pragma unroll 16
-            for (int b = lo; b < hi; ++b) {
-                const uint32_t c = uint32_t(a.counts[int64_t(b) * E + e]);
-                tot += c;
-                bef += b < int(blockIdx.x) ? c : 0u;
-            }
-            part[0][tid] = bef;
-            part[1][tid] = tot;
-        }
-        __syncthreads();
-        if (tid < E)
+        if (tid < E) {
+#pragma unroll 8
             for (int i = 0; i < groups; ++i) {
-                before += part[0][i * ep + tid];
-                total += part[1][i * ep + tid];
+                before += part[0][i * vecs * 8 + tid];
+                total += part[1][i * vecs * 8 + tid];
             }
+        }
     } else if (tid < E) {
 #pragma unroll
         for (int w = 0; w < kRW; ++w) total += cnt[w][tid];
@@ -228,7 +280,7 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     __syncthreads();
     for (int64_t i0 = t_lo * K; i0 < t_hi * K; i0 += 64) {
         const int64_t i = i0 + lane;
-        const int32_t e = i < t_hi * K ? a.ids[i] : -1;
+        const int32_t e = PHASE == 2 && i0 == t_lo * K ? id : slot_id(i);
         uint64_t same = __builtin_amdgcn_ballot_w64(e >= 0);
 #pragma unroll
         for (int b = 0; (1 << b) < kMaxExperts; ++b) {
@@ -249,8 +301,8 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
         }
     }
     // rows behind the last expert's
-    const int64_t lo = tb * K, hi = min(tb + a.per_block, a.tokens) * K;
-    for (int64_t i = lo + tid; i < hi; i += kRT)
+    const int64_t end = min(tb + a.per_block, a.tokens) * K;
+    for (int64_t i = tb * K + tid; i < end; i += kRT)
         if (i >= int64_t(all)) a.order[i] = -1;
 }
 
@@ -278,21 +330,33 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 
 void route_blocks(int64_t tokens, int32_t* blocks, int32_t* per_block) {
     const int64_t per = ((tokens + kMaxBlocks - 1) / kMaxBlocks + 63) / 64 * 64;
-    *per_block = int32_t(per > 64 ? per : 64);
+    *per_block = int32_t(std::min<int64_t>(std::max<int64_t>(per, 64), 65472));   // counts fit 16 bits
     const int64_t n = (tokens + *per_block - 1) / *per_block;
     *blocks = int32_t(n > 1 ? n : 1);                      // no tokens: one block writes the offsets
 }
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+namespace {
+template <int V>
+hipError_t launch(const RouteArgs& a, hipStream_t s) {
     if (a.blocks == 1) {
-        route_kernel<0><<<1, kRT, 0, s>>>(a);
+        route_kernel<0, V><<<1, kRT, 0, s>>>(a);
         return hipGetLastError();
     }
-    route_kernel<1><<<unsigned(a.blocks), kRT, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
+    route_kernel<1, V><<<unsigned(a.blocks), kRT, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_kernel<2><<<unsigned(a.blocks), kRT, 0, s>>>(a);
+    route_kernel<2, 1><<<unsigned(a.blocks), kRT, 0, s>>>(a);
     return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+    if (a.experts <= 16) return launch<1>(a, s);
+    if (a.experts <= 32) return launch<2>(a, s);
+    if (a.experts <= 64) return launch<4>(a, s);
+    if (a.experts <= 128) return launch<8>(a, s);
+    if (a.experts <= 256) return launch<16>(a, s);
+    return launch<32>(a, s);
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {
