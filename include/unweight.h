@@ -471,11 +471,19 @@ int64_t uw_moe_route_scratch_bytes(int64_t tokens, int experts, int top_k);
  * bounds the rows (out has n), x_rows those of X.  Rows of out outside every
  * expert's are left as they were.  Offsets that do not ascend within 0..n
  * are clamped and an index outside X reads row 0: no access leaves the
- * arrays.  Experts without rows cost nothing. */
+ * arrays.  Experts without rows cost nothing.
+ * scratch: NULL, or uw_grouped_scratch_bytes() bytes, which compressed weights
+ * of experts with hundreds of rows take as bf16; without it they are rebuilt
+ * tile by tile, slower.  Results with and without it agree to rounding.  Calls
+ * that share it must be ordered. */
 int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t rows, int64_t cols,
                     const uint16_t* X, int64_t x_rows, int64_t ldx,
                     const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
-                    void* out, int out_type, int64_t ldo, void* stream);
+                    void* out, int out_type, int64_t ldo,
+                    void* scratch, uint64_t scratch_bytes, void* stream);
+
+/* Scratch of uw_gemm_grouped (pair: of uw_moe_gate_up) or an error code. */
+int64_t uw_grouped_scratch_bytes(int compressed, int pair, int experts, int64_t rows, int64_t cols, int64_t n);
 
 /* The gate/up pair grouped by expert, h[s] = bf16(SiLU(G_e . x) * (U_e . x)),
  * rows and inputs as uw_gemm_grouped's; gate and up both bf16 or both
@@ -484,7 +492,8 @@ int uw_moe_gate_up(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t
                    int experts, int64_t rows, int64_t cols,
                    const uint16_t* X, int64_t x_rows, int64_t ldx,
                    const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
-                   uint16_t* h, int64_t ldh, void* stream);
+                   uint16_t* h, int64_t ldh,
+                   void* scratch, uint64_t scratch_bytes, void* stream);
 
 /* out[t] = sum_j weights[t][j] * Y[place[t][j]] + residual[t] over the j with
  * 0 <= place < n, in ascending j; Y fp32 [n, cols], residual may be NULL and
@@ -497,8 +506,9 @@ int uw_moe_combine(const float* Y, int64_t n, int64_t cols, const int32_t* place
  * the weighted sum, out[t] = sum_j w_j down_e(h_tj) + residual[t].  gate and up
  * [experts*rows, cols], down [experts*cols, rows], rows and cols multiples of
  * 64; residual may be NULL; out may be X or the residual (same stride and
- * type as the residual).  scratch: uw_moe_scratch_bytes() bytes; calls that
- * share it must be ordered. */
+ * type as the residual).  scratch: uw_moe_scratch_bytes() bytes (compressed:
+ * whether a weight is; with what it says for bf16 weights a call runs too, see
+ * uw_gemm_grouped); calls that share it must be ordered. */
 int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* up_w, const uw_dmat* up_d,
                  const uint16_t* down_w, const uw_dmat* down_d,
                  int experts, int64_t rows, int64_t cols,
@@ -507,7 +517,8 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
                  const void* residual, int residual_type, int64_t ldr,
                  void* out, int out_type, int64_t ldo,
                  void* scratch, uint64_t scratch_bytes, void* stream);
-int64_t uw_moe_scratch_bytes(int64_t tokens, int experts, int top_k, int64_t rows, int64_t cols);
+int64_t uw_moe_scratch_bytes(int compressed, int64_t tokens, int experts, int top_k, int64_t rows,
+                             int64_t cols);
 
 /* ----------------------------------------------------------- kernel timer */
 /* (API) Per-launch durations of the matmul kernels (GEMV and MFMA), for measuring

@@ -434,6 +434,15 @@ def _elsewhere(dev, stream):
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev))
 
 
+def _scratch_arg(scratch):
+    """(its pointer, its bytes)"""
+    if scratch is None:
+        return None, 0
+    if not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous")
+    return scratch.data_ptr() or None, scratch.numel() * scratch.element_size()
+
+
 def _out_arg(out, rows, cols, dtype, dev):
     """(out, row stride, type), allocated where it is None."""
     torch = _torch()
@@ -475,7 +484,7 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
         need = lib().uw_linear_scratch_bytes(0 if d is None else 1, rows, cols, batch)
         if need > 0:
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-    sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())
+    sp, sb = _scratch_arg(scratch)
     check(lib().uw_linear(w, d, rows, cols, X.data_ptr(), ldx, batch, None if bias is None else bias.data_ptr(),
                           UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type, ldr,
                           out.data_ptr(), out_type, ldo, sp, sb, _current_stream(dev)), "uw_linear")
@@ -503,7 +512,7 @@ def moe_route(logits, top_k, renormalize=True, scratch=None, stream=None) -> Rou
                 torch.empty((tokens, top_k), dtype=torch.float32, device=dev),
                 torch.empty(experts + 1, dtype=i32, device=dev), torch.empty(tokens * top_k, dtype=i32, device=dev),
                 torch.empty((tokens, top_k), dtype=i32, device=dev))
-    sp, sb = (None, 0) if scratch is None else (scratch.data_ptr(), scratch.numel() * scratch.element_size())
+    sp, sb = _scratch_arg(scratch)
     check(lib().uw_moe_route(logits.data_ptr(), kind, ld, tokens, experts, top_k, 1 if renormalize else 0,
                              r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(),
                              r.place.data_ptr(), sp, sb, _current_stream(dev)), "uw_moe_route")
@@ -521,33 +530,47 @@ def _group_args(X, offsets, order):
     return offsets.shape[0] - 1, order.shape[0]
 
 
-def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, stream=None):
+def _grouped_scratch(scratch, d, pair, experts, rows, cols, n, dev):
+    """(the tensor, its pointer, its bytes)"""
+    if scratch is None and d is not None and n > 512:
+        need = lib().uw_grouped_scratch_bytes(1, pair, experts, rows, cols, n)
+        if need < 0:
+            check(int(need), "uw_grouped_scratch_bytes")
+        if need:
+            scratch = _torch().empty(need, dtype=_torch().uint8, device=dev)
+    return (scratch, *_scratch_arg(scratch))
+
+
+def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, scratch=None,
+                 stream=None):
     """uw_gemm_grouped: rows offsets[e] .. offsets[e+1]-1 of the result are
     X's rows (order[s] // top_k where order is given, else s) times expert e's
-    matrix.  W [experts, rows, cols] or a DeviceMatrix of experts*rows rows."""
-    dev = _one_device(X, W, offsets, order, out)
+    matrix.  W [experts, rows, cols] or a DeviceMatrix of experts*rows rows.
+    `scratch` (None: allocated where it helps) is a tensor of any size."""
+    dev = _one_device(X, W, offsets, order, out, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return gemm_grouped(W, X, offsets, order, top_k, out, out_dtype)
+            return gemm_grouped(W, X, offsets, order, top_k, out, out_dtype, scratch)
     experts, n = _group_args(X, offsets, order)
     w, d, rows, cols = _weight_arg(W, experts)
     ldx = _x_arg(X, cols)
     out, ldo, out_type = _out_arg(out, n, rows, out_dtype, dev)
+    scratch, sp, sb = _grouped_scratch(scratch, d, 0, experts, rows, cols, n, dev)
     check(lib().uw_gemm_grouped(w, d, experts, rows, cols, X.data_ptr(), X.shape[0], ldx, offsets.data_ptr(),
                                 None if order is None else order.data_ptr(), top_k, n, out.data_ptr(), out_type, ldo,
-                                _current_stream(dev)), "uw_gemm_grouped")
+                                sp, sb, _current_stream(dev)), "uw_gemm_grouped")
     return out
 
 
-def moe_gate_up(gate, up, X, offsets, order=None, top_k=1, h=None, stream=None):
-    """uw_moe_gate_up: h = bf16(SiLU(x . gate_e^T) * (x . up_e^T)), rows and
-    inputs as gemm_grouped's."""
-    dev = _one_device(X, gate, up, offsets, order, h)
+def moe_gate_up(gate, up, X, offsets, order=None, top_k=1, h=None, scratch=None, stream=None):
+    """uw_moe_gate_up: h = bf16(SiLU(x . gate_e^T) * (x . up_e^T)), rows,
+    inputs and scratch as gemm_grouped's."""
+    dev = _one_device(X, gate, up, offsets, order, h, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return moe_gate_up(gate, up, X, offsets, order, top_k, h)
+            return moe_gate_up(gate, up, X, offsets, order, top_k, h, scratch)
     experts, n = _group_args(X, offsets, order)
     gw, gd, rows, cols = _weight_arg(gate, experts, "gate")
     uw_, ud, urows, ucols = _weight_arg(up, experts, "up")
@@ -555,9 +578,10 @@ def moe_gate_up(gate, up, X, offsets, order=None, top_k=1, h=None, stream=None):
         raise ValueError("gate and up must have the same shape")
     ldx = _x_arg(X, cols)
     h, ldh, kind = _out_arg(h, n, rows, _torch().bfloat16, dev)
+    scratch, sp, sb = _grouped_scratch(scratch, gd, 1, experts, rows, cols, n, dev)
     check(lib().uw_moe_gate_up(gw, gd, uw_, ud, experts, rows, cols, X.data_ptr(), X.shape[0], ldx, offsets.data_ptr(),
                                None if order is None else order.data_ptr(), top_k, n, h.data_ptr(), ldh,
-                               _current_stream(dev)), "uw_moe_gate_up")
+                               sp, sb, _current_stream(dev)), "uw_moe_gate_up")
     return h
 
 
@@ -584,8 +608,8 @@ def moe_combine(Y, place, weights, residual=None, out=None, out_dtype=None, stre
     return out
 
 
-def moe_scratch_bytes(tokens, experts, top_k, rows, cols) -> int:
-    n = lib().uw_moe_scratch_bytes(tokens, experts, top_k, rows, cols)
+def moe_scratch_bytes(tokens, experts, top_k, rows, cols, compressed=False) -> int:
+    n = lib().uw_moe_scratch_bytes(1 if compressed else 0, tokens, experts, top_k, rows, cols)
     if n < 0:
         check(int(n), "uw_moe_scratch_bytes")
     return int(n)
@@ -615,11 +639,11 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     res, res_type, ldr = _residual_arg(residual, tokens, H)
     out, ldo, out_type = _out_arg(out, tokens, H, out_dtype, dev)
     if scratch is None:
-        scratch = torch.empty(moe_scratch_bytes(tokens, experts, top_k, F, H), dtype=torch.uint8, device=dev)
+        scratch = torch.empty(moe_scratch_bytes(tokens, experts, top_k, F, H, bool(gd or dd)), dtype=torch.uint8, device=dev)
+    sp, sb = _scratch_arg(scratch)
     check(lib().uw_moe_layer(gw, gd, uw_, ud, dw, dd, experts, F, H, X.data_ptr(), ldx, tokens, logits.data_ptr(), kind,
                              ldl, top_k, 1 if renormalize else 0, res, res_type, ldr, out.data_ptr(), out_type, ldo,
-                             scratch.data_ptr(), scratch.numel() * scratch.element_size(), _current_stream(dev)),
-          "uw_moe_layer")
+                             sp, sb, _current_stream(dev)), "uw_moe_layer")
     return out
 
 

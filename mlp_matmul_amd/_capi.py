@@ -92,12 +92,15 @@ SIGNATURES = {
     "uw_linear_scratch_bytes": (_I64, [_INT, _I64, _I64, _I64]),
     "uw_moe_route": (_INT, [_P, _INT, _I64, _I64, _INT, _INT, _INT, _P, _P, _P, _P, _P, _P, _U64, _P]),
     "uw_moe_route_scratch_bytes": (_I64, [_I64, _INT, _INT]),
-    "uw_gemm_grouped": (_INT, [_P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _INT, _I64, _P]),
-    "uw_moe_gate_up": (_INT, [_P, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _I64, _P]),
+    "uw_gemm_grouped": (_INT, [_P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _INT, _I64, _P,
+                                _U64, _P]),
+    "uw_grouped_scratch_bytes": (_I64, [_INT, _INT, _INT, _I64, _I64, _I64]),
+    "uw_moe_gate_up": (_INT, [_P, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _P, _INT, _I64, _P, _I64, _P, _U64,
+                               _P]),
     "uw_moe_combine": (_INT, [_P, _I64, _I64, _P, _P, _I64, _INT, _P, _INT, _I64, _P, _INT, _I64, _P]),
     "uw_moe_layer": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _INT, _I64, _INT, _INT, _P,
                              _INT, _I64, _P, _INT, _I64, _P, _U64, _P]),
-    "uw_moe_scratch_bytes": (_I64, [_I64, _INT, _INT, _I64, _I64]),
+    "uw_moe_scratch_bytes": (_I64, [_INT, _I64, _INT, _INT, _I64, _I64]),
     "uw_kernel_timer_enable": (_INT, [_INT]),
     "uw_kernel_timer_disable": (_INT, []),
     "uw_kernel_timer_reset": (_INT, []),

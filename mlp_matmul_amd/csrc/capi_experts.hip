@@ -101,6 +101,19 @@ int check_epilogue(const uwk::Epilogue& e, int64_t n, int64_t rows, const void* 
     return UW_OK;
 }
 
+// Optional scratch, which nothing else may lie in.
+int check_scratch(const void* scratch, uint64_t* bytes, const uwk::Epilogue& e, int64_t n, int64_t rows, const void* X,
+                  uint64_t x_bytes, const char* who) {
+    if (!aligned16(scratch)) return bad(who, "misaligned scratch");
+    if (!scratch) *bytes = 0;
+    if (overlap(e.out, span(n, rows, e.ldo, value_bytes(e.out_type)), scratch, *bytes) ||
+        overlap(X, x_bytes, scratch, *bytes) ||
+        (e.residual && overlap(e.residual, span(n, rows, e.ldr, value_bytes(e.residual_type)), scratch, *bytes)) ||
+        (e.bias && overlap(e.bias, uint64_t(rows) * value_bytes(e.bias_type), scratch, *bytes)))
+        return bad(who, "the scratch overlaps an input or out");
+    return UW_OK;
+}
+
 int check_groups(int experts, int64_t n, const int32_t* offsets, const int32_t* order, int top_k, int64_t x_rows,
                  const char* who) {
     if (experts < 1 || experts > uwk::kMaxExperts) return bad(who, "experts must be 1..512");
@@ -148,10 +161,11 @@ int check_routing(int64_t tokens, int experts, int top_k, const char* who) {
 
 // Scratch of a whole layer.
 struct LayerLayout {
-    uint64_t ids, weights, offsets, order, place, route, h, y, total;
+    uint64_t ids, weights, offsets, order, place, route, h, y, total;   // total: what a call cannot do without
+    uint64_t expand;                                                    // behind it: room for expanded weights
 };
 
-LayerLayout layer_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t F, int64_t H) {
+LayerLayout layer_layout(bool pal, int64_t tokens, int experts, int64_t top_k, int64_t F, int64_t H) {
     LayerLayout l{};
     const uint64_t slots = uint64_t(tokens) * uint64_t(top_k);
     uint64_t off = 0;
@@ -169,6 +183,8 @@ LayerLayout layer_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t
     l.h = take(slots * uint64_t(F) * 2);
     l.y = take(slots * uint64_t(H) * 4);
     l.total = off;
+    l.expand = std::max(uwk::grouped_scratch(pal, true, experts, F, H, int64_t(slots)),
+                        uwk::grouped_scratch(pal, false, experts, H, F, int64_t(slots)));
     return l;
 }
 
@@ -203,10 +219,7 @@ int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols, c
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {bias, residual, out, ldr, ldo, bias_type, residual_type, out_type, act};
         if ((rc = check_epilogue(a.ep, batch, rows, X, span(batch, cols, ldx, 2), who))) return rc;
-        if (!aligned16(scratch)) return bad(who, "misaligned scratch");
-        if (!scratch) scratch_bytes = 0;
-        if (overlap(out, span(batch, rows, ldo, value_bytes(out_type)), scratch, scratch_bytes))
-            return bad(who, "out overlaps the scratch");
+        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, batch, rows, X, span(batch, cols, ldx, 2), who))) return rc;
         const hipError_t e = uwk::launch_linear(d != nullptr, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
@@ -249,9 +262,24 @@ int uw_moe_route(const void* logits, int logits_type, int64_t ld, int64_t tokens
     });
 }
 
+int64_t uw_grouped_scratch_bytes(int compressed, int pair, int experts, int64_t rows, int64_t cols, int64_t n) {
+    int64_t out = 0;
+    const int rc = guarded([&]() -> int {
+        const char* who = "uw_grouped_scratch_bytes";
+        if (experts < 1 || experts > uwk::kMaxExperts) return bad(who, "experts must be 1..512");
+        if (rows < 0 || cols < uw::kGroup || n < 0 || n >= (int64_t(1) << 31) || cols % uw::kGroup)
+            return bad(who, "bad argument (cols must be a positive multiple of 64)");
+        if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows * cols >= (int64_t(1) << 31))
+            return fail(UW_EUNSUPPORTED, std::string(who) + ": a matrix of 2^31 weights or more");
+        out = int64_t(uwk::grouped_scratch(compressed != 0, pair != 0, experts, rows, cols, n));
+        return UW_OK;
+    });
+    return rc ? rc : out;
+}
+
 int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t rows, int64_t cols, const uint16_t* X,
                     int64_t x_rows, int64_t ldx, const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
-                    void* out, int out_type, int64_t ldo, void* stream) {
+                    void* out, int out_type, int64_t ldo, void* scratch, uint64_t scratch_bytes, void* stream) {
     return guarded([&]() -> int {
         const char* who = "uw_gemm_grouped";
         int rc = check_groups(experts, n, offsets, order, top_k, x_rows, who);
@@ -262,7 +290,8 @@ int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t ro
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {nullptr, nullptr, out, 0, ldo, UW_F32, UW_F32, out_type, UW_ACT_NONE};
         if ((rc = check_epilogue(a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
-        const hipError_t e = uwk::launch_grouped(d != nullptr, false, a, as_stream(stream));
+        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
+        const hipError_t e = uwk::launch_grouped(d != nullptr, false, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
 }
@@ -270,7 +299,7 @@ int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t ro
 int uw_moe_gate_up(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* up_w, const uw_dmat* up_d,
                    int experts, int64_t rows, int64_t cols, const uint16_t* X, int64_t x_rows, int64_t ldx,
                    const int32_t* offsets, const int32_t* order, int top_k, int64_t n, uint16_t* h, int64_t ldh,
-                   void* stream) {
+                   void* scratch, uint64_t scratch_bytes, void* stream) {
     return guarded([&]() -> int {
         const char* who = "uw_moe_gate_up";
         int rc = check_groups(experts, n, offsets, order, top_k, x_rows, who);
@@ -283,7 +312,8 @@ int uw_moe_gate_up(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {nullptr, nullptr, h, 0, ldh, UW_F32, UW_F32, UW_BF16, UW_ACT_NONE};
         if ((rc = check_epilogue(a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
-        const hipError_t e = uwk::launch_grouped(gate_d != nullptr, true, a, as_stream(stream));
+        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
+        const hipError_t e = uwk::launch_grouped(gate_d != nullptr, true, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
 }
@@ -310,7 +340,7 @@ int uw_moe_combine(const float* Y, int64_t n, int64_t cols, const int32_t* place
     });
 }
 
-int64_t uw_moe_scratch_bytes(int64_t tokens, int experts, int top_k, int64_t rows, int64_t cols) {
+int64_t uw_moe_scratch_bytes(int compressed, int64_t tokens, int experts, int top_k, int64_t rows, int64_t cols) {
     int64_t out = 0;
     const int rc = guarded([&]() -> int {
         const char* who = "uw_moe_scratch_bytes";
@@ -319,7 +349,8 @@ int64_t uw_moe_scratch_bytes(int64_t tokens, int experts, int top_k, int64_t row
         if (rows < uw::kGroup || cols < uw::kGroup || rows % uw::kGroup || cols % uw::kGroup ||
             rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31))
             return bad(who, "rows and cols must be positive multiples of 64");
-        out = int64_t(layer_layout(tokens, experts, top_k, rows, cols).total);
+        const LayerLayout l = layer_layout(compressed != 0, tokens, experts, top_k, rows, cols);
+        out = int64_t(l.total + l.expand);
         return UW_OK;
     });
     return rc ? rc : out;
@@ -349,11 +380,10 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         // out is written by the last step alone: it may be X or the residual
         const uwk::Epilogue ep{nullptr, residual, out, ldr, ldo, UW_F32, residual_type, out_type, UW_ACT_NONE};
         if ((rc = check_epilogue(ep, tokens, cols, nullptr, 0, who))) return rc;
-        const LayerLayout l = layer_layout(tokens, experts, top_k, rows, cols);
+        const LayerLayout l = layer_layout(gate_d || down_d, tokens, experts, top_k, rows, cols);
         if (!scratch || !aligned16(scratch) || scratch_bytes < l.total)
             return bad(who, "scratch smaller than uw_moe_scratch_bytes()");
-        if (overlap(out, span(tokens, cols, ldo, value_bytes(out_type)), scratch, l.total))
-            return bad(who, "out overlaps the scratch");
+        if ((rc = check_scratch(scratch, &scratch_bytes, ep, tokens, cols, X, span(tokens, cols, ldx, 2), who))) return rc;
         uint8_t* const base = static_cast<uint8_t*>(scratch);
         int32_t* const ids = reinterpret_cast<int32_t*>(base + l.ids);
         float* const weights = reinterpret_cast<float*>(base + l.weights);
@@ -362,12 +392,14 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         int32_t* const place = reinterpret_cast<int32_t*>(base + l.place);
         uint16_t* const h = reinterpret_cast<uint16_t*>(base + l.h);
         float* const y = reinterpret_cast<float*>(base + l.y);
+        void* const room = base + l.total;
+        const uint64_t room_bytes = scratch_bytes - l.total;
         const int64_t n = tokens * top_k;
         if ((rc = uw_moe_route(logits, logits_type, ldl, tokens, experts, top_k, renormalize, ids, weights, offsets,
                                order, place, base + l.route, l.h - l.route, stream)))
             return rc;
         if ((rc = uw_moe_gate_up(gate_w, gate_d, up_w, up_d, experts, rows, cols, X, tokens, ldx, offsets, order,
-                                 top_k, n, h, rows, stream)))
+                                 top_k, n, h, rows, room, room_bytes, stream)))
             return rc;
         if (tokens == 1) {                      // a single token's sum needs no array of the experts' outputs
             uwk::GroupArgs a = group_args(h, n, rows, offsets, nullptr, 1, n, experts, cols, rows);
@@ -380,7 +412,7 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
             }
         }
         if ((rc = uw_gemm_grouped(down_w, down_d, experts, cols, rows, h, n, rows, offsets, nullptr, 1, n, y, UW_F32,
-                                  cols, stream)))
+                                  cols, room, room_bytes, stream)))
             return rc;
         return uw_moe_combine(y, n, cols, place, weights, tokens, top_k, residual, residual_type, ldr, out, out_type,
                               ldo, stream);

@@ -65,7 +65,8 @@ uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int
 // The epilogue matmul: a.n rows of X in order, no offsets.
 hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s);
 // A product grouped by expert, or the gate/up pair.
-hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s);
+hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s);
+uint64_t grouped_scratch(bool pal, bool pair, int experts, int64_t rows, int64_t cols, int64_t n);
 
 // The kernels behind them.  One or two rows an expert, cols <= 24576 / rows:
 bool gemv_rows_supported(const GroupArgs& a, int nb);

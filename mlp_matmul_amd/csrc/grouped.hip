@@ -71,14 +71,16 @@ TilePlan plan_tiles(bool pair, double groups, double rows, bool exact, bool may_
 }
 
 // ------------------------------------------------------------ direct palette to bf16
-// 16 weights a lane; a lane's 16 columns lie in one 64-weight group.  Memory
-// bound: 1.53 bytes read and 2 written a weight.
-__global__ __launch_bounds__(256) void expand_kernel(Weight w, int64_t n, uint16_t* out) {
+// n weights of each expert (blockIdx.y) that has rows, 16 a lane; a lane's 16
+// columns lie in one 64-weight group.  Memory bound: 1.53 bytes read and 2
+// written a weight.
+__global__ __launch_bounds__(256) void expand_kernel(Weight w, int64_t n, const int32_t* offsets, uint16_t* out) {
     __shared__ uint32_t lut[256];
+    if (offsets && offsets[blockIdx.y + 1] <= offsets[blockIdx.y]) return;
     lut[threadIdx.x] = (pal_byte(w.pal, threadIdx.x & 15) << 7) | (pal_byte(w.pal, threadIdx.x >> 4) << 23);
     __syncthreads();
-    const int64_t pos = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 16;
-    if (pos >= n) return;
+    const int64_t in = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 16, pos = int64_t(blockIdx.y) * n + in;
+    if (in >= n) return;
     const u32x2_t nib = load_stream8(static_cast<const uint8_t*>(w.w) + pos / 2);
     const u32x4_t sm = load_stream16(w.sm + pos);
     const int64_t g = pos >> 6;
@@ -126,6 +128,19 @@ MatArgs mat_args(const GroupArgs& a) {
     for (int i = 0; i < 4; ++i) m.pal[i] = a.w[0].pal[i];
     m.split_k = 1;
     return m;
+}
+
+// The experts' weights (one matrix's) as bf16 at `out`.
+uint64_t expanded_bytes(const GroupArgs& a) {
+    return (uint64_t(a.E) * uint64_t(a.R) * uint64_t(a.C) * 2 + 255) & ~uint64_t(255);
+}
+
+hipError_t expand(const GroupArgs& a, Weight* w, uint16_t* out, hipStream_t s) {
+    const int64_t n = int64_t(a.R) * a.C;
+    expand_kernel<<<dim3(unsigned((n / 16 + 255) / 256), unsigned(a.E)), 256, 0, s>>>(*w, n, a.offsets, out);
+    *w = Weight{};
+    w->w = out;
+    return hipGetLastError();
 }
 
 // What a large batch of palette weights does: nothing special, K-slices of the
@@ -188,7 +203,12 @@ hipError_t linear_tiles(const GroupArgs& a, void* scratch, uint64_t scratch_byte
     return e != hipSuccess || plan.split == 1 ? e : add_sums(a, b.sums, plan.split, s);
 }
 
-uint64_t expanded_bytes(const GroupArgs& a) { return (uint64_t(a.R) * uint64_t(a.C) * 2 + 255) & ~uint64_t(255); }
+// Whether palette weights of experts with so many rows on average are expanded
+// (512 is where it pays):
+// with 530 rows of 4 experts' 4096 x 4096 138 us against 169 rebuilding tile by
+// tile, gate/up of 8 experts' 1024 x 2048 96 against 96; with 2000 rows 335
+// against 484 and 201 against 276.
+bool expand_groups(const GroupArgs& a) { return a.n > 512 * std::min<int64_t>(a.n, a.E); }
 
 }  // namespace
 
@@ -197,6 +217,7 @@ uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int
     a.R = int32_t(rows);
     a.C = int32_t(cols);
     a.n = batch;
+    a.E = 1;
     a.cus = cus;
     if (rows == 0 || few_rows(a)) return 0;
     const PalPlan p = pal ? pal_plan(a) : PLAN_TILES;
@@ -213,14 +234,9 @@ hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t s
     if (!pal) return linear_tiles(a, scratch, scratch_bytes, s);
     const PalPlan plan = pal_plan(a);
     if (plan == PLAN_EXPAND && scratch_bytes >= expanded_bytes(a)) {
-        const int64_t n = int64_t(a.R) * a.C;
-        uint16_t* const w = static_cast<uint16_t*>(scratch);
-        expand_kernel<<<unsigned((n / 16 + 255) / 256), 256, 0, s>>>(a.w[0], n, w);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
         GroupArgs b = a;
-        b.w[0] = Weight{};
-        b.w[0].w = w;
+        const hipError_t e = expand(a, &b.w[0], static_cast<uint16_t*>(scratch), s);
+        if (e != hipSuccess) return e;
         return linear_tiles(b, static_cast<uint8_t*>(scratch) + expanded_bytes(a), scratch_bytes - expanded_bytes(a), s);
     }
     if (plan == PLAN_SUMS && a.ldx == a.C) {
@@ -238,7 +254,16 @@ hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t s
     return launch_tile_pal(false, a, units <= 8 * int64_t(a.cus) ? PAL_TILE_64x64 : PAL_TILE_128x128, s);
 }
 
-hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s) {
+uint64_t grouped_scratch(bool pal, bool pair, int experts, int64_t rows, int64_t cols, int64_t n) {
+    GroupArgs a{};
+    a.R = int32_t(rows);
+    a.C = int32_t(cols);
+    a.E = experts;
+    a.n = n;
+    return pal && rows && n && expand_groups(a) ? expanded_bytes(a) * (pair ? 2 : 1) : 0;
+}
+
+hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s) {
     if (a.n <= 0 || a.R <= 0) return hipSuccess;
     const int64_t groups = std::min<int64_t>(a.n, a.E);
     const double rows = double(a.n) / double(groups);
@@ -254,6 +279,14 @@ hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, hipStream_t s
     if (rows <= (pal ? 1.5 : 2.5)) return launch_skinny_rows(pal, pair, a, 4, s);
     if (rows <= (pal ? 11 : 14)) return launch_skinny_rows(pal, pair, a, 16, s);
     if (!pal) return launch_tile(pair, a, plan_tiles(pair, double(groups), rows, false, false, a).shape, s);
+    if (expand_groups(a) && scratch_bytes >= expanded_bytes(a) * (pair ? 2 : 1)) {
+        GroupArgs b = a;
+        for (int m = 0; m < (pair ? 2 : 1); ++m) {
+            const hipError_t e = expand(a, &b.w[m], static_cast<uint16_t*>(scratch) + uint64_t(m) * (expanded_bytes(a) / 2), s);
+            if (e != hipSuccess) return e;
+        }
+        return launch_tile(pair, b, plan_tiles(pair, double(groups), rows, false, false, b).shape, s);
+    }
     // 25 rows of 8 experts: 128 x 64 tiles 111 us, 128 x 128 123; 64 rows: 151
     // and 122
     return launch_tile_pal(pair, a, rows <= 40 ? PAL_TILE_128x64 : PAL_TILE_128x128, s);

@@ -33,14 +33,14 @@ def route(**kw):
 
 def grouped(**kw):
     a = dict(w=at(1), d=None, experts=4, rows=64, cols=128, X=at(2), xr=20, ldx=128, off=at(3), order=at(4), top_k=2,
-             n=40, out=at(5), ot=0, ldo=64, stream=None)
+             n=40, out=at(5), ot=0, ldo=64, scratch=None, sb=0, stream=None)
     a.update(kw)
     return uw.lib().uw_gemm_grouped(*a.values())
 
 
 def gate_up(**kw):
     a = dict(gw=at(1), gd=None, uw_=at(2), ud=None, experts=4, rows=64, cols=128, X=at(3), xr=20, ldx=128, off=at(4),
-             order=at(5), top_k=2, n=40, h=at(6), ldh=64, stream=None)
+             order=at(5), top_k=2, n=40, h=at(6), ldh=64, scratch=None, sb=0, stream=None)
     a.update(kw)
     return uw.lib().uw_moe_gate_up(*a.values())
 
@@ -138,8 +138,16 @@ def test_scratch_sizes():
     assert L.uw_moe_route_scratch_bytes(65, 256, 8) == 2 * 256 * 2
     assert L.uw_moe_route_scratch_bytes(1 << 24, 16, 8) == 8448          # 257 blocks of 32 bytes, up to 256
     assert L.uw_moe_route_scratch_bytes(1, 0, 1) == _capi.UW_EINVAL
-    assert L.uw_moe_scratch_bytes(3, 8, 2, 64, 128) == 256 * 5 + 6 * 64 * 2 + 6 * 128 * 4
-    assert L.uw_moe_scratch_bytes(3, 8, 2, 60, 128) == _capi.UW_EINVAL
+    assert L.uw_moe_scratch_bytes(0, 3, 8, 2, 64, 128) == 256 * 5 + 6 * 64 * 2 + 6 * 128 * 4
+    assert L.uw_moe_scratch_bytes(0, 3, 8, 2, 60, 128) == _capi.UW_EINVAL
+    assert L.uw_moe_scratch_bytes(1, 3, 8, 2, 64, 128) == L.uw_moe_scratch_bytes(0, 3, 8, 2, 64, 128)
+    assert (L.uw_moe_scratch_bytes(1, 1100, 2, 1, 64, 128) ==
+            L.uw_moe_scratch_bytes(0, 1100, 2, 1, 64, 128) + 2 * 2 * 64 * 128 * 2)
+    assert L.uw_grouped_scratch_bytes(1, 1, 4, 64, 128, 512 * 4) == 0
+    assert L.uw_grouped_scratch_bytes(1, 1, 4, 64, 128, 512 * 4 + 1) == 2 * 4 * 64 * 128 * 2
+    assert L.uw_grouped_scratch_bytes(1, 0, 0, 64, 128, 5) == _capi.UW_EINVAL
+    assert L.uw_grouped_scratch_bytes(1, 0, 4, 64, 100, 5) == _capi.UW_EINVAL
+    assert L.uw_grouped_scratch_bytes(1, 0, 4, 1 << 20, 1 << 11, 5) == _capi.UW_EUNSUPPORTED
     assert L.uw_linear_scratch_bytes(1, 64, 100, 4) == _capi.UW_EINVAL
     assert L.uw_linear_scratch_bytes(1, 1 << 20, 1 << 11, 4) == _capi.UW_EUNSUPPORTED
     assert L.uw_linear_scratch_bytes(1, 4096, 4096, 32) == 0
@@ -149,6 +157,15 @@ def test_scratch_sizes():
     assert L.uw_linear_scratch_bytes(0, 4096, 14336, 64) % (64 * 4096 * 4) == 0
     assert L.uw_linear_scratch_bytes(0, 4096, 14336, 64) > 0
     assert L.uw_linear_scratch_bytes(1, 4096, 4096, 100) % (100 * 4096 * 4) == 0
+
+
+def test_scratch_refusals():
+    """Scratch that is misaligned or lies in an input or the output."""
+    for f, x, out in ((linear, 2, 5), (grouped, 2, 5), (gate_up, 3, 6)):
+        for kw in (dict(scratch=at(9) + 8, sb=1 << 10), dict(scratch=at(x), sb=1 << 10), dict(scratch=at(out), sb=1 << 10)):
+            assert f(**kw) == _capi.UW_EINVAL, (f, kw)
+            assert b"scratch" in uw.lib().uw_last_error()
+    assert linear(scratch=at(3), sb=16) == linear(scratch=at(4), sb=16) == _capi.UW_EINVAL
 
 
 def test_from_sections_refusals():

@@ -174,6 +174,39 @@ def test_linear_infinities(torch_cuda):
             assert not bool(out[-1].isfinite().logical_and(out[-1] != 0).any())
 
 
+def scratches(torch, need):
+    """None (the call takes its own), none at all, too little and exactly enough, full of NaN."""
+    return [None] + [torch.full((k,), 255, dtype=torch.uint8).cuda() for k in sorted({0, max(need - 16, 0), need})]
+
+
+@pytest.mark.parametrize("pal", [False, True])
+@pytest.mark.parametrize("rows,cols,batch", [(130, 4096, 40), (4099, 1024, 100), (1000, 14336, 130), (260, 128, 70),
+                                             (300, 2048, 600), (516, 4096, 1300), (4096, 576, 2050)])
+def test_linear_scratch(torch_cuda, rows, cols, batch, pal):
+    """Slices of K, tails and expanded weights: any scratch gives the result; rows are checked at both ends."""
+    torch = torch_cuda
+    W, w = make_weight(torch, rows, 1, rows, cols, pal)
+    need = uw.lib().uw_linear_scratch_bytes(int(pal), rows, cols, batch)
+    g = torch.Generator().manual_seed(batch)
+    bias = torch.randn(rows, generator=g).cuda()
+    at = torch.arange(batch) if batch <= 200 else torch.cat([torch.arange(70), torch.arange(batch - 70, batch)])
+    for pad in (0, 8):
+        X = rows_of(torch, batch, batch, cols, pad)
+        res = torch.randn(batch, rows + pad, generator=g).bfloat16().cuda()[:, :rows]
+        x = f64(X)[at]
+        v, err = x @ w[0].t() + f64(bias), sum_bound(torch, x, w[0])
+        y = activate(torch, v, "gelu")
+        want = y + f64(res)[at]
+        err = 1.13 * (err + v.abs() * 2.0 ** -23) + 2.0 ** -20 * (v.abs() + y.abs()) + want.abs() * 2.0 ** -23
+        for s in scratches(torch, need):
+            what = f"linear scratch {batch}x{rows}x{cols} pal={pal} pad={pad} {None if s is None else s.numel()} of {need}"
+            print_case(what)
+            out = torch.full((batch, rows + 4), 7.0).cuda()
+            uw.linear(W if pal else W[0], X, bias=bias, act="gelu", residual=res, out=out[:, :rows], scratch=s)
+            check(torch, out[at.cuda(), :rows], want, err, what)
+            assert bool(out.isfinite().all()) and bool((out[:, rows:] == 7).all())
+
+
 # ------------------------------------------------------------------- routing
 def plain_route(logits, top_k, renorm):
     l = logits.astype(np.float64).copy()
@@ -328,6 +361,35 @@ def test_grouped_weights_exact(torch_cuda):
             assert torch.equal(out, w[e, :, at])
 
 
+def test_grouped_scratch(torch_cuda):
+    """Experts with hundreds of rows: any scratch gives the result, an expert without rows is not expanded."""
+    torch = torch_cuda
+    counts, rows, cols = [900, 0, 600, 701], 130, 320
+    (W, w), (U, u) = (make_weight(torch, 50 + i, 4, rows, cols, True, 0.02) for i in range(2))
+    off, order, n = grouping(torch, 8, counts, 2, 1000)
+    X = rows_of(torch, 5, 1000, cols, 8)
+    at = torch.cat([torch.arange(0, n, 17), off[1:].cpu().long() - 1])
+    e = torch.from_numpy(np.repeat(np.arange(4), counts))[at]
+    x = f64(X)[order.cpu().long()[at] // 2]
+    v, q = [torch.bmm(m[e], x[:, :, None])[:, :, 0] for m in (w, u)]
+    err, err_q = [(cols + 8) * 2.0 ** -23 * torch.bmm(m[e].abs(), x.abs()[:, :, None])[:, :, 0] for m in (w, u)]
+    s = activate(torch, v, "silu")
+    err_s = 1.13 * err + 2.0 ** -20 * (v.abs() + s.abs())
+    L = uw.lib()
+    for pair in (0, 1):
+        need = L.uw_grouped_scratch_bytes(1, pair, 4, rows, cols, n)
+        assert need >= (1 + pair) * 4 * rows * cols * 2 and L.uw_grouped_scratch_bytes(0, pair, 4, rows, cols, n) == 0
+        for t in scratches(torch, need):
+            what = f"grouped scratch pair={pair} {None if t is None else t.numel()} of {need}"
+            print_case(what)
+            if pair:
+                h = uw.moe_gate_up(W, U, X, off, order, 2, scratch=t)
+                check(torch, h[at.cuda()], s * q, err_s * (q.abs() + err_q) + s.abs() * err_q +
+                      (s * q).abs() * 2.0 ** -23, what)
+            else:
+                check(torch, uw.gemm_grouped(W, X, off, order, 2, scratch=t)[at.cuda()], v, err, what)
+
+
 def test_grouped_bad_offsets_stay_inside(torch_cuda):
     """Offsets out of order or out of range and indexes outside X: rows outside the output's are untouched."""
     torch = torch_cuda
@@ -392,7 +454,7 @@ def layer_reference(torch, g, u, d, x, logits, top_k, renorm, residual):
 
 @pytest.mark.parametrize("pal", [False, True])
 @pytest.mark.parametrize("tokens,experts,top_k", [(1, 8, 2), (2, 4, 4), (7, 16, 3), (33, 8, 2), (70, 100, 2),
-                                                  (150, 5, 1)])
+                                                  (150, 5, 1), (1100, 2, 1)])
 def test_layer(torch_cuda, tokens, experts, top_k, pal):
     """The whole layer, padded tokens among the others, with and without a
     residual; the single calls in a row give the same result."""
