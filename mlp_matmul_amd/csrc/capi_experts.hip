@@ -72,6 +72,7 @@ int take_weight(const uint16_t* w, const uw_dmat* d, int64_t experts, int64_t ro
     out->bitmap = d->bitmap;
     out->tile_vbase = d->tile_vbase;
     uw::pack_palette(d->palette, out->pal);
+    out->last_slot = d->verbatim_groups ? uint32_t(d->verbatim_groups) - 1 : 0;
     return UW_OK;
 }
 

@@ -22,6 +22,7 @@ struct Weight {
     const uint64_t* bitmap;
     const uint32_t* tile_vbase;
     uint32_t pal[4];
+    uint32_t last_slot;         // of the verbatim groups (0 without any): lanes without one read inside VEXP
 };
 
 // y = act(v + bias[r]) + residual[b][r], rounded once to the type of `out`.

@@ -111,7 +111,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a,
         for (int m = 0; m < M; ++m) {
             word[m] = a.w[m].bitmap[min(t0 + lane, tl)];
             base[m] = a.w[m].tile_vbase[min(t0 + lane, tl)];
-            ebase[m] = a.w[m].tile_vbase[first >> 12];
+            ebase[m] = min(a.w[m].tile_vbase[first >> 12], a.w[m].last_slot);
         }
     }
     float bias = 0.f, residual[NB] = {};                     // of the next row to finish; lane 0 uses them
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_combine_kernel(GroupArgs
         const uint64_t tl = min((g >> 6) + uint32_t(lane) % tiles, (g + (C >> 6) - 1) >> 6);
         word = w.bitmap[tl];
         base = w.tile_vbase[tl];
-        ebase = w.tile_vbase[first_of(uint32_t(id < 0 || id >= a.E ? 0 : id)) >> 12];   // lane j: expert j's
+        ebase = min(w.tile_vbase[first_of(uint32_t(id < 0 || id >= a.E ? 0 : id)) >> 12], w.last_slot);   // lane j: expert j's
         lut[tid] = (pal_byte(w.pal, uint32_t(tid) & 15u) << 7) | (pal_byte(w.pal, uint32_t(tid) >> 4) << 23);
     }
     struct Pos {

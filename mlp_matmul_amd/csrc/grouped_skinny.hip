@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(GroupArgs a, uint32_t b
             const int64_t end = g0 + min(2 * s1, C / 64u) - 1;         // the segment's last group
             const uint64_t w0 = mat(r).bitmap[g >> 6], w1 = mat(r).bitmap[max(g, end) >> 6];
             const uint32_t before = mat(r).tile_vbase[g >> 6];
-            base[r] = mat(r).tile_vbase[first >> 12];                  // uniform: slots below are the expert's own
+            base[r] = min(mat(r).tile_vbase[first >> 12], mat(r).last_slot);   // uniform: slots below are the expert's own
             const uint32_t bit = (uint32_t(g) & 63u) + (q >> 1);       // may be 64: the next word's first
             slot[r] = before - base[r] + uint32_t(__popcll(bit > 63u ? w0 : w0 & ((uint64_t(1) << bit) - 1)));
             uint64_t lo = bit > 63u ? w1 : (bit ? (w0 >> bit) | (w1 << (64u - bit)) : w0);

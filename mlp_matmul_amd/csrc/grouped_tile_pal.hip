@@ -76,7 +76,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void tile_pal_kernel(GroupArgs a, 
             const int64_t g0 = (first + int64_t(wrow[it]) * C) >> 6, g = g0 + min(s0, steps - 1u);
             const int64_t end = g0 + min(s0 + 64u, steps) - 1;
             const uint64_t w0 = w.bitmap[g >> 6], w1 = w.bitmap[max(g, end) >> 6];
-            base[it] = w.tile_vbase[first >> 12];
+            base[it] = min(w.tile_vbase[first >> 12], w.last_slot);
             const uint32_t bit = uint32_t(g) & 63u;
             slot[it] = w.tile_vbase[g >> 6] - base[it] + uint32_t(__popcll(w0 & ((uint64_t(1) << bit) - 1)));
             uint64_t lo = bit ? (w0 >> bit) | (w1 << (64u - bit)) : w0;

@@ -361,6 +361,35 @@ def test_grouped_weights_exact(torch_cuda):
             assert torch.equal(out, w[e, :, at])
 
 
+def test_grouped_verbatim_in_the_first_expert_only(torch_cuda):
+    """Experts behind the last verbatim group, with every number of rows an expert."""
+    torch = torch_cuda
+    experts, rows, cols = 4, 64, 256
+    w = workloads.gaussian_weights(np.random.default_rng(5), experts * rows, cols, 0.02, 0.05, 1.0)
+    w[rows:] = 0x3F00 | (w[rows:] & 0x807F)                # one exponent: all of these groups are palette groups
+    c = uw.compress(w)
+    assert c.info().verbatim_groups > 0
+    W = c.to_device(uw.DIRECT_SECTIONS)
+    exact = f64(torch.from_numpy(w.view(np.int16)).view(torch.bfloat16)).view(experts, rows, cols)
+    for per in (1, 3, 9, 30, 70):
+        print_case(f"grouped without verbatim groups at the end, {per} rows an expert")
+        X = rows_of(torch, per, experts * per, cols)
+        off = torch.arange(experts + 1, dtype=torch.int32).cuda() * per
+        x = f64(X).view(experts, per, cols)
+        want = torch.bmm(x, exact.transpose(1, 2).contiguous()).view(-1, rows)
+        bound = (cols + 8) * 2.0 ** -23 * torch.bmm(x.abs(), exact.abs().transpose(1, 2).contiguous()).view(-1, rows)
+        check(torch, uw.gemm_grouped(W, X, off), want, bound, "products")
+        if per == 1:
+            logits = torch.tensor([[0.0, 1.0, 2.0, 3.0]]).cuda()
+            r = uw.moe_route(logits, 2)
+            h = rows_of(torch, 9, 2, cols)
+            y = uw.gemm_grouped(W, h, r.offsets)
+            e = r.ids[0].cpu().long()
+            hx = f64(h)[r.place[0].cpu().long()]
+            check(torch, y[r.place[0].long()], torch.stack([hx[j] @ exact[e[j]].t() for j in range(2)]),
+                  torch.stack([(cols + 8) * 2.0 ** -23 * (hx[j].abs() @ exact[e[j]].abs().t()) for j in range(2)]), "routed")
+
+
 def test_grouped_scratch(torch_cuda):
     """Experts with hundreds of rows: any scratch gives the result, an expert without rows is not expanded."""
     torch = torch_cuda
