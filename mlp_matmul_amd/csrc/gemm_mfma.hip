@@ -478,16 +478,6 @@ bool mfma_supported(const MatArgs& a) {
     return a.C % kKS == 0 && (a.C == 0 || table_bytes(a) <= 48 * 1024);
 }
 
-hipError_t launch_mfma_sums(int src, const MatArgs& a, hipStream_t s) {
-    if (!mfma_supported(a)) return hipErrorNotSupported;
-    if (lds_gemm_preferred(src, a)) return launch_lds_gemm(src, a, s);
-    switch (src) {
-        case SRC_BF16: return launch_src<SRC_BF16>(a, s);
-        case SRC_EXP: return launch_src<SRC_EXP>(a, s);
-        default: return launch_src<SRC_PAL>(a, s);
-    }
-}
-
 hipError_t launch_mfma(int src, const MatArgs& a, hipStream_t s) {
     if (a.R == 0 || a.B == 0) return hipSuccess;
     if (a.C == 0) {                                    // empty sums
@@ -495,7 +485,14 @@ hipError_t launch_mfma(int src, const MatArgs& a, hipStream_t s) {
         zero_fill<<<unsigned((n + 255) / 256), 256, 0, s>>>(a.Y, n);
         return hipGetLastError();
     }
-    const hipError_t e = launch_mfma_sums(src, a, s);
+    if (!mfma_supported(a)) return hipErrorNotSupported;
+    hipError_t e;
+    if (lds_gemm_preferred(src, a)) e = launch_lds_gemm(src, a, s);
+    else switch (src) {
+        case SRC_BF16: e = launch_src<SRC_BF16>(a, s); break;
+        case SRC_EXP: e = launch_src<SRC_EXP>(a, s); break;
+        default: e = launch_src<SRC_PAL>(a, s); break;
+    }
     if (e != hipSuccess || a.split_k <= 1) return e;
     const int64_t n = a.B * a.R;
     splitk_reduce<<<unsigned((n + 255) / 256), 256, 0, s>>>(a.partial, a.split_k, n, a.Y);

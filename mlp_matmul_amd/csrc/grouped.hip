@@ -147,15 +147,16 @@ hipError_t expand(const GroupArgs& a, Weight* w, uint16_t* out, hipStream_t s) {
 // tiled matmul into scratch, or the weights expanded to bf16 there.
 enum PalPlan { PLAN_TILES, PLAN_SUMS, PLAN_EXPAND };
 
-// Through 512 rows the tiled matmuls of gemm_mfma.hip and gemm_lds.hip, which
-// split K, with their sums in scratch and the epilogue in the kernel that adds
-// them (14336 x 4096, 64 rows: 36 us against 45 for the 64 x 64 tiles); above,
-// the weights are expanded once and the bf16 tiles run at twice the rate of
-// the rebuilding ones (4096 x 4096 x 2049 rows: 14 + 72 us against 156).
+// Through 512 rows the tiled matmul of gemm_lds.hip, which splits K, with its
+// sums in scratch and the epilogue in the kernel that adds them (14336 x 4096,
+// 64 rows: 33 us against 45 for the 64 x 64 tiles); above, the weights are
+// expanded once and the bf16 tiles run at twice the rate of the rebuilding ones
+// (4096 x 4096 x 2049 rows: 14 + 72 us against 156; at 400 rows of 4096 x 14336
+// expanding costs 46 us of 112, the sums take 90).
 PalPlan pal_plan(const GroupArgs& a) {
     if (a.n > 512) return PLAN_EXPAND;
     const MatArgs m = mat_args(a);
-    return mfma_supported(m) && a.n * a.C < (int64_t(1) << 31) && a.n * a.R < (int64_t(1) << 31) ? PLAN_SUMS
+    return lds_gemm_supported(SRC_PAL, m) && a.n * a.C < (int64_t(1) << 31) && a.n * a.R < (int64_t(1) << 31) ? PLAN_SUMS
                                                                                                  : PLAN_TILES;
 }
 
@@ -221,7 +222,7 @@ uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int
     a.cus = cus;
     if (rows == 0 || few_rows(a)) return 0;
     const PalPlan p = pal ? pal_plan(a) : PLAN_TILES;
-    if (p == PLAN_SUMS) return sums_bytes(a, mfma_default_split(SRC_PAL, mat_args(a), cus));
+    if (p == PLAN_SUMS) return sums_bytes(a, lds_gemm_default_split(SRC_PAL, mat_args(a), cus));
     if (pal && p == PLAN_TILES) return 0;
     const TilePlan t = plan_tiles(false, 1, double(a.n), true, true, a);
     return (p == PLAN_EXPAND ? expanded_bytes(a) : 0) + (t.split > 1 ? sums_bytes(a, t.split) : 0);
@@ -241,10 +242,10 @@ hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t s
     }
     if (plan == PLAN_SUMS && a.ldx == a.C) {
         MatArgs m = mat_args(a);
-        m.split_k = mfma_default_split(SRC_PAL, m, a.cus);
+        m.split_k = lds_gemm_default_split(SRC_PAL, m, a.cus);
         if (sums_bytes(a, m.split_k) <= scratch_bytes) {
             m.Y = m.partial = static_cast<float*>(scratch);
-            const hipError_t e = launch_mfma_sums(SRC_PAL, m, s);
+            const hipError_t e = launch_lds_gemm(SRC_PAL, m, s);
             return e == hipSuccess ? add_sums(a, m.partial, m.split_k, s) : e;
         }
     }

@@ -59,9 +59,6 @@ hipError_t launch_gemv(int src, const MatArgs& a, hipStream_t s);
 bool gemv_gateup_supported(const MatArgs& gate, const MatArgs& up);
 hipError_t launch_gemv_gateup(const MatArgs& gate, const MatArgs& up, uint16_t* h, hipStream_t s);
 hipError_t launch_mfma(int src, const MatArgs& a, hipStream_t s);
-// The same without the last step: the K-slices' sums in a.partial when split_k
-// > 1 (else the products in a.Y).  R, C and B above 0.
-hipError_t launch_mfma_sums(int src, const MatArgs& a, hipStream_t s);
 bool mfma_supported(const MatArgs& a);
 // Split-K that fills the chip for the tiled MFMA family on `cus` compute units.
 int mfma_default_split(int src, const MatArgs& a, int cus);
