@@ -13,6 +13,9 @@
 // rows touch, one tile a lane; an item picks its 16 flags by lane reads, so
 // flags and slots cost scalar instructions, and the raw exponents come with
 // the item's other loads (lanes outside verbatim groups share one line).
+//   Measured: gate/up of one token, two experts of 3584 x 4096, palette, 20 us
+// for 90 MB, the read rate but for 5 us of launch and first loads; 1024 x 4096
+// 5.7 us, nothing but those.
 #include "grouped_common.h"
 #include "kernels.h"
 

@@ -1,15 +1,22 @@
 // Many rows per expert (or a large batch of the epilogue matmul): the matrix
 // units bound the product.  bf16 weights.
 //
-// A workgroup of four waves, one per SIMD, multiplies MT weight rows with NT
-// input rows in steps of 64 columns.  Both tiles go from memory to LDS by
-// global_load_lds, double-buffered.  A wave owns a (MT/2) x (NT/2) block of
-// the output: with 128 x 128 it reads 16 fragments of 1 KB for 64 MFMAs of 16
-// cycles, half the LDS's rate.  Fragments of the next 32 columns are read into
-// a second register set while the MFMAs of these run.  One barrier a step, in
-// its middle: by then every wave has the step's last fragments in registers
-// and its own loads of the next step have landed, so the step's buffers can
-// be refilled.
+// A workgroup multiplies MT weight rows with NT input rows in steps of 64
+// columns.  Both tiles go from memory to LDS by global_load_lds, S steps of
+// them there or on their way.  A wave owns a (MT/WM) x (NT/2) block of the
+// output: 64 x 64 with 256 x 128 tiles and eight waves, 16 fragments of 1 KB
+// from LDS for 64 MFMAs of 16 cycles: the LDS and the matrix units are equally
+// busy; 64 x 128 with 256 x 256, three quarters of the LDS's time.  Fragments
+// of the next 32 columns are read into a second register set while the MFMAs
+// of these run.  One barrier a step, in its middle: by then every wave has the
+// step's last fragments in registers and its own loads of the next step have
+// landed, so the step's buffers can be refilled.
+//   8192 x 8192 x 8192: 916 us with 256 x 256 (1200 TFLOP/s), 984 with
+// 256 x 128, 1362 with 128 x 64, 2424 with 64 x 64; small products have too few
+// of the large ones for every compute unit, and waste less of the small ones
+// behind an expert's last row.  128 x 128 tiles, one or two a compute unit, were
+// no better than 256 x 128 (4000 tokens of 8 experts: 101 against 96 us; 3000 of
+// 64: 190 and 184).
 //   Rows of a tile are 128 bytes in LDS; 16-byte chunk c of row r sits at
 // position c ^ (r & 7) ^ (r >> 3 & 1), which makes the fragment reads (16 rows,
 // one chunk column) free of bank conflicts while four lanes of a load still
@@ -156,7 +163,10 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
         __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
-    for (int i = 0; i < S; ++i) load(uint32_t(i), i);
+    for (int i = 0; i < S; ++i) {
+        load(uint32_t(i), i);
+        __builtin_amdgcn_sched_barrier(0);               // in this order: the waits count them
+    }
     wait<(S - 1) * (WD + XD)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
