@@ -427,7 +427,7 @@ enum {                                             /* activations, in fp32 */
 /* out[b][r] = act(sum_c X[b][c] W[r][c] + bias[r]) + residual[b][r].
  * bias [rows] and residual [batch, rows] may be NULL; out may be the residual
  * itself (same pointer, stride and type), and overlaps nothing else.
- * scratch: NULL, or uw_linear_scratch_bytes() bytes (0 through 16 rows) for
+ * scratch: NULL, or uw_linear_scratch_bytes() bytes (0 through 2 rows) for
  * sums of K-slices, where they fill the chip, and for large batches of
  * compressed weights the matrix as bf16; with less than that K is not split and
  * the weights are rebuilt tile by tile, slower.  Calls that share it must be

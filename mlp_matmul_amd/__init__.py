@@ -480,7 +480,7 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
         raise ValueError(f"bias must be a contiguous [{rows}] tensor")
     res, res_type, ldr = _residual_arg(residual, batch, rows)
     out, ldo, out_type = _out_arg(out, batch, rows, out_dtype, dev)
-    if scratch is None and batch > 16:                       # never any through 16 rows
+    if scratch is None and batch > 2:                        # never any through 2 rows
         need = lib().uw_linear_scratch_bytes(0 if d is None else 1, rows, cols, batch)
         if need > 0:
             scratch = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -532,7 +532,7 @@ def _group_args(X, offsets, order):
 
 def _grouped_scratch(scratch, d, pair, experts, rows, cols, n, dev):
     """(the tensor, its pointer, its bytes)"""
-    if scratch is None and d is not None and n > 512:
+    if scratch is None and d is not None and n > 64:         # it may help some rows later
         need = lib().uw_grouped_scratch_bytes(1, pair, experts, rows, cols, n)
         if need < 0:
             check(int(need), "uw_grouped_scratch_bytes")

@@ -184,8 +184,8 @@ LayerLayout layer_layout(bool pal, int64_t tokens, int experts, int64_t top_k, i
     l.h = take(slots * uint64_t(F) * 2);
     l.y = take(slots * uint64_t(H) * 4);
     l.total = off;
-    l.expand = std::max(uwk::grouped_scratch(pal, true, experts, F, H, int64_t(slots)),
-                        uwk::grouped_scratch(pal, false, experts, H, F, int64_t(slots)));
+    l.expand = std::max(uwk::grouped_scratch(pal, true, experts, F, H, int64_t(slots), uw::device_cus()),
+                        uwk::grouped_scratch(pal, false, experts, H, F, int64_t(slots), uw::device_cus()));
     return l;
 }
 
@@ -272,7 +272,7 @@ int64_t uw_grouped_scratch_bytes(int compressed, int pair, int experts, int64_t 
             return bad(who, "bad argument (cols must be a positive multiple of 64)");
         if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows * cols >= (int64_t(1) << 31))
             return fail(UW_EUNSUPPORTED, std::string(who) + ": a matrix of 2^31 weights or more");
-        out = int64_t(uwk::grouped_scratch(compressed != 0, pair != 0, experts, rows, cols, n));
+        out = int64_t(uwk::grouped_scratch(compressed != 0, pair != 0, experts, rows, cols, n, uw::device_cus()));
         return UW_OK;
     });
     return rc ? rc : out;

@@ -67,7 +67,7 @@ uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int
 hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s);
 // A product grouped by expert, or the gate/up pair.
 hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s);
-uint64_t grouped_scratch(bool pal, bool pair, int experts, int64_t rows, int64_t cols, int64_t n);
+uint64_t grouped_scratch(bool pal, bool pair, int experts, int64_t rows, int64_t cols, int64_t n, int cus);
 
 // The kernels behind them.  One or two rows an expert, cols <= 24576 / rows:
 bool gemv_rows_supported(const GroupArgs& a, int nb);
@@ -78,10 +78,11 @@ bool gemv_combine_supported(const GroupArgs& a, int top_k);
 hipError_t launch_gemv_combine(bool pal, const GroupArgs& a, const CombineArgs& c, hipStream_t s);
 // Up to `rows` (4, 16 or 32) rows an expert before its weights are read again.
 hipError_t launch_skinny_rows(bool pal, bool pair, const GroupArgs& a, int rows, hipStream_t s);
+int skinny_waves(bool pair, int rows, const GroupArgs& a);    // of its workgroups
 // Tiles of weight rows x input rows, bf16 and palette.
 enum TileShape { TILE_64x64, TILE_128x64, TILE_256x128, TILE_256x256, TILE_SHAPES };
 hipError_t launch_tile(bool pair, const GroupArgs& a, TileShape shape, hipStream_t s);
-enum PalTileShape { PAL_TILE_64x64, PAL_TILE_128x64, PAL_TILE_128x128 };
+enum PalTileShape { PAL_TILE_64x64, PAL_TILE_128x64, PAL_TILE_128x128, PAL_TILE_SHAPES };
 hipError_t launch_tile_pal(bool pair, const GroupArgs& a, PalTileShape shape, hipStream_t s);
 
 struct RouteArgs {

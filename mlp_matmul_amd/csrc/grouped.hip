@@ -16,60 +16,6 @@ namespace uwk {
 
 namespace {
 
-// A tile shape's time for one 64-column step of a round of workgroups, in us on
-// MI355X: with a workgroup here and there, with one on each compute unit, and
-// with `per_cu` on each.
-struct TileCost {
-    int mt, nt, per_cu;
-    double few, one, full;
-};
-constexpr TileCost kTiles[TILE_SHAPES] = {{64, 64, 2, 0.16, 0.265, 0.51},
-                                          {128, 64, 2, 0.34, 0.45, 0.86},
-                                          {256, 128, 1, 0.65, 0.96, 0.96},
-                                          {256, 256, 1, 1.2, 1.7, 1.7}};
-// A launch with its first loads and its stores, bytes a us from memory and the
-// share of them that a second reading of the weights or the rows costs, and the
-// kernel that adds slices, with the bytes a us of writing and reading them.
-constexpr double kLaunchUs = 6, kBytesUs = 7.8e6, kWeightsAgain = 0.45, kRowsAgain = 0.33, kSumsUs = 2, kSumsBytesUs = 3.9e6;
-
-struct TilePlan {
-    TileShape shape;
-    int split;
-    double us;
-};
-
-// The tile shape and number of K-slices for `groups` products of `rows` input
-// rows each with [R, C]: the choice of the least estimated time, which is the
-// rounds of workgroups that the chip takes or the bytes from memory, whichever
-// is longer.  The constants are fitted to the 16 choices at 32 sizes (1000 x
-// 2048 to 14336 x 4096 and 4096 x 14336, 33 to 2049 rows); what it picks there is
-// the fastest choice or within 8% of it.  At 4096 x 14336, us, against 64 x 64
-// tiles without slices: 64 rows 31 (128 x 64, 8 slices) and 73, 256 rows 48
-// (256 x 128, 8) and 72, 800 rows 106 (256 x 128, 2) and 198.
-TilePlan plan_tiles(bool pair, double groups, double rows, bool exact, bool may_split, const GroupArgs& a) {
-    TilePlan best{TILE_64x64, 1, 1e30};
-    const double weights = groups * double(a.R) * double(a.C) * (pair ? 4 : 2);
-    for (int i = 0; i < TILE_SHAPES; ++i) {
-        const TileCost& c = kTiles[i];
-        const int mt = pair ? c.mt / 2 : c.mt;
-        const double bands = groups * double((a.R + mt - 1) / mt);
-        // tiles of an expert: the rows are spread, half a tile is lost on average
-        const double tiles = exact ? double((int64_t(rows) + c.nt - 1) / c.nt) : std::max(1.0, rows / c.nt + 0.5);
-        const double again = kWeightsAgain * weights * (tiles - 1) + kRowsAgain * bands * rows * double(a.C) * 2;
-        for (int split = 1; split <= (may_split ? 8 : 1) && split * 2 <= std::max(2, a.C / 64); split *= 2) {
-            const double per = bands * tiles * split / a.cus;          // workgroups a compute unit
-            const double rounds = double(int64_t(per / c.per_cu)), rest = per - rounds * c.per_cu;
-            double round = rounds * c.full;
-            if (rest > 1) round += c.one + (c.full - c.one) * (rest - 1);
-            else if (rest > 0) round += c.few + (c.one - c.few) * rest;
-            double us = kLaunchUs + std::max(round * double(a.C / 64) / split, (weights + again) / kBytesUs);
-            if (split > 1) us += kSumsUs + split * rows * double(a.R) * 8 / kSumsBytesUs;
-            if (us < best.us) best = {TileShape(i), split, us};
-        }
-    }
-    return best;
-}
-
 // ------------------------------------------------------------ direct palette to bf16
 // n weights of each expert (blockIdx.y) that has rows, 16 a lane; a lane's 16
 // columns lie in one 64-weight group.  Memory bound: 1.53 bytes read and 2
@@ -108,8 +54,8 @@ __global__ __launch_bounds__(256) void sums_epilogue_kernel(const float* sums, i
     if (i >= B * quads) return;
     const int64_t b = i / quads;
     const int r = int(i % quads) * 4;
-    f32x4_t v = load4(sums, VT_F32, b * R + r, r, R, (R & 3) == 0);
-    for (int z = 1; z < split; ++z) v += load4(sums, VT_F32, (z * B + b) * R + r, r, R, (R & 3) == 0);
+    f32x4_t v = load4(sums, VT_F32, b * R + r, r, R);
+    for (int z = 1; z < split; ++z) v += load4(sums, VT_F32, (z * B + b) * R + r, r, R);
     epilogue4(ep, b, r, R, v);
 }
 
@@ -143,28 +89,6 @@ hipError_t expand(const GroupArgs& a, Weight* w, uint16_t* out, hipStream_t s) {
     return hipGetLastError();
 }
 
-// What a large batch of palette weights does: nothing special, K-slices of the
-// tiled matmul into scratch, or the weights expanded to bf16 there.
-enum PalPlan { PLAN_TILES, PLAN_SUMS, PLAN_EXPAND };
-
-// Through 512 rows the tiled matmul of gemm_lds.hip, which splits K, with its
-// sums in scratch and the epilogue in the kernel that adds them (14336 x 4096,
-// 64 rows: 33 us against 45 for the 64 x 64 tiles); above, the weights are
-// expanded once and the bf16 tiles run at twice the rate of the rebuilding ones
-// (4096 x 4096 x 2049 rows: 14 + 72 us against 156; at 400 rows of 4096 x 14336
-// expanding costs 46 us of 112, the sums take 90).
-PalPlan pal_plan(const GroupArgs& a) {
-    if (a.n > 512) return PLAN_EXPAND;
-    const MatArgs m = mat_args(a);
-    return lds_gemm_supported(SRC_PAL, m) && a.n * a.C < (int64_t(1) << 31) && a.n * a.R < (int64_t(1) << 31) ? PLAN_SUMS
-                                                                                                 : PLAN_TILES;
-}
-
-// Whether n rows are left to the skinny kernel: through 16, and through 32 on
-// matrices below 2^25 weights (24 rows of 4096 x 4096: 10 us against 13; of
-// 14336 x 4096: 34 against 29, palette 40 against 33).
-bool few_rows(const GroupArgs& a) { return a.n <= 16 || (a.n <= 32 && int64_t(a.R) * a.C < (int64_t(1) << 25)); }
-
 uint64_t sums_bytes(const GroupArgs& a, int split) { return uint64_t(split) * uint64_t(a.n) * uint64_t(a.R) * 4; }
 
 hipError_t add_sums(const GroupArgs& a, const float* sums, int split, hipStream_t s) {
@@ -173,124 +97,243 @@ hipError_t add_sums(const GroupArgs& a, const float* sums, int split, hipStream_
     return hipGetLastError();
 }
 
-// bf16 tiles.  A few rows behind the last whole tile go to the skinny kernel
-// where they would start another round of tiles (2049 rows of 4096 x 4096: 61 +
-// 9 us against 95).
-hipError_t linear_tiles(const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s) {
-    TilePlan plan = plan_tiles(false, 1, double(a.n), true, true, a);
-    if (plan.split > 1 && sums_bytes(a, plan.split) > scratch_bytes) plan = plan_tiles(false, 1, double(a.n), true, false, a);
+// ------------------------------------------------------------ which kernel
+// The choice goes by estimated times.  The constants below are fitted to 746
+// sizes of both weight forms (one matrix of 64 x 64 to 16000 x 14000 with 3 to
+// 2500 rows, the pair and the single product of 2 to 64 experts with 3 to 900
+// rows each, even and skewed), each timed on MI355X with every kernel; what the
+// estimates choose there takes 1.02 to 1.04 times the fastest kernel's time in
+// the geometric mean, by kind of product, and 1.7 times at worst.  Thresholds
+// on the rows alone took 1.05 to 1.21 times.
+
+// Times in us: a 64-column step of a round of workgroups with one here and
+// there, with one on each compute unit, with `per_cu` on each; the launch, and
+// what a round needs before its first step and behind its last, in steps.  Bytes a us
+// of the weight stream where that takes longer, and the share of it that a
+// further tile of rows costs: tiles of one band run side by side and find part
+// of its weights in a cache.
+struct TileCost {
+    int mt, nt, per_cu;
+    double few, one, full, launch, around, stream, again;
+};
+constexpr TileCost kTiles[TILE_SHAPES] = {{64, 64, 2, 0.18, 0.28, 0.45, 4.8, 6.2, 4.8e6, 0.53},
+                                          {128, 64, 2, 0.31, 0.48, 0.67, 4.6, 5.5, 5.1e6, 0.43},
+                                          {256, 128, 1, 0.63, 0.88, 0.88, 4.8, 7.6, 4.9e6, 0.30},
+                                          {256, 256, 1, 1.1, 1.5, 1.5, 6.3, 6.1, 5.7e6, 1.1}};
+constexpr TileCost kPalTiles[PAL_TILE_SHAPES] = {{64, 64, 3, 0.52, 0.62, 0.97, 4.6, 5.3, 3.3e6, 0.73},
+                                                 {128, 64, 2, 0.71, 0.90, 1.1, 3.1, 6.8, 3.1e6, 0.64},
+                                                 {128, 128, 2, 0.93, 1.1, 1.7, 6.1, 3.2, 2.9e6, 0.80}};
+constexpr double kFillUnits = 1.5;             // the stream is at its full rate from 1 / 1.5 workgroups a compute unit on
+// The skinny kernel: a wave's step of 128 columns with few waves and with the
+// chip full of them; the rest as above, in us.
+struct SkinnyCost {
+    double few, full, launch, around, stream, again;
+};
+constexpr int kSkinnyRows[3] = {4, 16, 32};
+constexpr SkinnyCost kSkinny[2][2][3] = {      // palette, pair, rows
+    {{{0.30, 0.30, 4.9, 0, 5.5e6, 0.34}, {0.43, 1.0, 3.8, 1.5, 4.3e6, 0}, {0.33, 0.80, 3.3, 2.1, 3.5e6, 0.40}},
+     {{0, 1.2, 3.4, 2.9, 5.6e6, 0}, {0, 0.85, 4.6, 2.9, 5.0e6, 0.36}, {0, 1.0, 3.9, 4.6, 5.6e6, 0.24}}},
+    {{{0.52, 2.2, 4.2, 2.1, 5.3e6, 0.14}, {0.66, 1.2, 3.8, 2.9, 3.9e6, 0.62}, {0.59, 1.0, 3.2, 3.4, 2.4e6, 0.30}},
+     {{0.37, 1.7, 3.2, 5.2, 3.8e6, 0.20}, {0.52, 1.2, 4.6, 4.1, 3.1e6, 0.34}, {0.29, 1.5, 7.4, 3.9, 3.0e6, 0.32}}}};
+// The tiled matmul of gemm_lds.hip into scratch: a step by its tiles' rows.
+constexpr double kSums[3] = {0.64, 1.0, 1.8}, kSumsLaunch = 6.9, kSumsAround = 2.3, kSumsStream = 5.5e6;
+// What expanding one matrix or a pair adds, and the bytes a us; the launch that
+// adds slices, and the bytes a us of writing and reading them.
+constexpr double kExpandLaunch[2] = {4.6, 6.9}, kExpandStream = 6.4e6, kAddLaunch = 3.1, kSliceStream = 5e6;
+
+struct Choice {
+    enum Kernel { SKINNY, TILE, PAL_TILE, SUMS, EXPAND } kernel;
+    int shape, split;
+    double us;
+};
+
+struct Problem {
+    bool pal, pair, exact;       // exact: one group, `rows` is no average
+    double groups, rows;
+    const GroupArgs& a;
+
+    double weights() const { return groups * double(a.R) * double(a.C) * (pair ? 2 : 1); }
+    // tiles of a group: with rows spread over the groups half a tile is lost on average
+    double tiles(int nt) const { return exact ? double((a.n + nt - 1) / nt) : std::max(1.0, rows / nt + 0.5); }
+};
+
+double slices_us(const GroupArgs& a, int split) { return split * double(a.n) * double(a.R) * 8 / kSliceStream; }
+
+double tile_us(const Problem& p, const TileCost& c, bool pal, int split) {
+    const int mt = p.pair ? c.mt / 2 : c.mt;
+    const double tiles = p.tiles(c.nt), bands = p.groups * double((p.a.R + mt - 1) / mt);
+    const double per = bands * tiles * split / p.a.cus;                // workgroups a compute unit
+    const double rounds = double(int64_t(per / c.per_cu)), rest = per - rounds * c.per_cu;
+    double step = rounds * c.full;
+    if (rest > 1) step += c.one + (c.full - c.one) * (rest - 1) / (c.per_cu - 1);
+    else if (rest > 0) step += c.few + (c.one - c.few) * rest;
+    const double stream = p.weights() * (pal ? 1.53 : 2) * (1 + c.again * (tiles - 1)) / c.stream /
+                          std::min(1.0, per * kFillUnits);
+    const double us = c.launch + std::max(step * (double(p.a.C / 64) / split + c.around), stream);
+    return split > 1 ? us + kAddLaunch + slices_us(p.a, split) : us;
+}
+
+double skinny_us(const Problem& p, int i) {
+    const SkinnyCost& c = kSkinny[p.pal][p.pair][i];
+    const int rows = kSkinnyRows[i], kw = skinny_waves(p.pair, rows, p.a);
+    const int slot = (p.pal ? 3 : 4) * (p.pair ? 2 : 1) + rows / 4;    // KB of a wave's step; two of them, 160 KB in all
+    const int per_cu = std::min(160 / (2 * kw * slot + 2), 32 / kw);
+    const double tiles = p.tiles(rows), units = p.groups * double((p.a.R + 15) / 16) * tiles;
+    const double rounds = units / p.a.cus / per_cu, steps = std::max(1.0, double(p.a.C / 64) / 2 / kw);
+    const double step = c.few + (c.full - c.few) * std::min(1.0, rounds);
+    return c.launch + std::max(std::max(1.0, rounds) * (steps * step + c.around),
+                               p.weights() * (p.pal ? 1.53 : 2) * (1 + c.again * (tiles - 1)) / c.stream);
+}
+
+// The tiled matmul of gemm_lds.hip, with its sums in scratch.
+bool sums_supported(const GroupArgs& a) {
+    return a.ldx == a.C && lds_gemm_supported(SRC_PAL, mat_args(a)) && a.n * a.C < (int64_t(1) << 31) &&
+           a.n * a.R < (int64_t(1) << 31);
+}
+
+int sums_split(const GroupArgs& a) { return lds_gemm_default_split(SRC_PAL, mat_args(a), a.cus); }
+
+double sums_us(const Problem& p) {
+    const int i = p.a.n <= 64 ? 0 : p.a.n <= 128 || p.a.R >= 8192 ? 1 : 2, nt = 64 << i, split = sums_split(p.a);
+    const int64_t per = (int64_t((p.a.R + 127) / 128) * ((p.a.n + nt - 1) / nt) * split + p.a.cus - 1) / p.a.cus;
+    return kSumsLaunch + std::max(double(per) * (kSums[i] * double(p.a.C / 64) / split + kSumsAround),
+                                  p.weights() * 1.53 / kSumsStream) +
+           slices_us(p.a, split);
+}
+
+// What a choice takes of the scratch.
+uint64_t choice_bytes(const Choice& c, bool pair, const GroupArgs& a) {
+    return (c.kernel == Choice::EXPAND ? expanded_bytes(a) * (pair ? 2 : 1) : 0) +
+           (c.kernel == Choice::SUMS || c.split > 1 ? sums_bytes(a, c.split) : 0);
+}
+
+// The fastest choice that the scratch allows.
+Choice choose(const Problem& p, uint64_t scratch_bytes) {
+    Choice best{Choice::SKINNY, 16, 1, 1e30};
+    auto offer = [&](Choice c) {
+        if (c.us < best.us && choice_bytes(c, p.pair, p.a) <= scratch_bytes) best = c;
+    };
+    for (int i = 0; i < 3; ++i) offer({Choice::SKINNY, kSkinnyRows[i], 1, skinny_us(p, i)});
+    for (int i = 0; i < (p.pair ? TILE_256x256 : TILE_SHAPES); ++i)
+        for (int split = 1; split <= (p.exact ? 8 : 1) && (split == 1 || split * 2 <= p.a.C / 64); split *= 2) {
+            const double us = tile_us(p, kTiles[i], false, split);
+            if (!p.pal) offer({Choice::TILE, i, split, us});
+            else offer({Choice::EXPAND, i, split, us + kExpandLaunch[p.pair] + p.weights() * 3.53 / kExpandStream});
+        }
+    if (p.pal)
+        for (int i = 0; i < PAL_TILE_SHAPES; ++i) offer({Choice::PAL_TILE, i, 1, tile_us(p, kPalTiles[i], true, 1)});
+    if (p.pal && p.exact && sums_supported(p.a)) offer({Choice::SUMS, 0, sums_split(p.a), sums_us(p)});
+    return best;
+}
+
+// bf16 tiles of one matrix.  A few rows behind the last whole tile go to the
+// skinny kernel where they would start another round of tiles (2049 rows of
+// 4096 x 4096: 61 + 9 us against 95).
+hipError_t linear_tiles(const GroupArgs& a, const Choice& c, void* sums, hipStream_t s) {
     const int64_t tail = a.n % 128;                      // 128 and 256 both divide what is left
     if (tail && tail <= 32 && a.n > 256) {
-        const TilePlan part = plan_tiles(false, 1, double(a.n - tail), true, false, a);
-        // the weights once more, and a launch
-        if (part.us + kLaunchUs + double(a.R) * double(a.C) * 2 / kBytesUs < plan.us) {
-            GroupArgs head = a, rest = a;
-            head.n = head.x_rows = a.n - tail;
-            rest.n = rest.x_rows = tail;
+        GroupArgs head = a, rest = a;
+        head.n = head.x_rows = a.n - tail;
+        rest.n = rest.x_rows = tail;
+        const Problem ph{false, false, true, 1, double(head.n), head}, pr{false, false, true, 1, double(tail), rest};
+        const Choice part = choose(ph, 0), last = choose(pr, 0);
+        const bool gemv = tail <= 2 && gemv_rows_supported(rest, int(tail));
+        const double whole = tile_us({false, false, true, 1, double(a.n), a}, kTiles[c.shape], false, c.split);
+        if (part.kernel == Choice::TILE && last.kernel == Choice::SKINNY && part.us + last.us < whole) {
             rest.X = a.X + head.n * a.ldx;
             const int64_t ob = a.ep.out_type == VT_BF16 ? 2 : 4, rb = a.ep.residual_type == VT_BF16 ? 2 : 4;
             rest.ep.out = static_cast<uint8_t*>(a.ep.out) + head.n * a.ep.ldo * ob;
             if (a.ep.residual) rest.ep.residual = static_cast<const uint8_t*>(a.ep.residual) + head.n * a.ep.ldr * rb;
-            const hipError_t e = launch_tile(false, head, part.shape, s);
+            const hipError_t e = launch_tile(false, head, TileShape(part.shape), s);
             if (e != hipSuccess) return e;
-            if (tail <= 2 && gemv_rows_supported(rest, int(tail))) return launch_gemv_rows(false, false, rest, int(tail), s);
-            return launch_skinny_rows(false, false, rest, int(tail), s);
+            return gemv ? launch_gemv_rows(false, false, rest, int(tail), s) : launch_skinny_rows(false, false, rest, last.shape, s);
         }
     }
     GroupArgs b = a;
-    b.split = plan.split;
-    b.sums = static_cast<float*>(scratch);
-    const hipError_t e = launch_tile(false, b, plan.shape, s);
-    return e != hipSuccess || plan.split == 1 ? e : add_sums(a, b.sums, plan.split, s);
+    b.split = c.split;
+    b.sums = static_cast<float*>(sums);
+    const hipError_t e = launch_tile(false, b, TileShape(c.shape), s);
+    return e != hipSuccess || c.split == 1 ? e : add_sums(a, b.sums, c.split, s);
 }
 
-// Whether palette weights of experts with so many rows on average are expanded
-// (512 is where it pays):
-// with 530 rows of 4 experts' 4096 x 4096 138 us against 169 rebuilding tile by
-// tile, gate/up of 8 experts' 1024 x 2048 96 against 96; with 2000 rows 335
-// against 484 and 201 against 276.
-bool expand_groups(const GroupArgs& a) { return a.n > 512 * std::min<int64_t>(a.n, a.E); }
+Problem linear_problem(bool pal, const GroupArgs& a) { return {pal, false, true, 1, double(a.n), a}; }
+
+Problem grouped_problem(bool pal, bool pair, const GroupArgs& a) {
+    const double groups = double(std::min<int64_t>(a.n, a.E));
+    return {pal, pair, false, groups, double(a.n) / groups, a};
+}
+
+// Sizes alone, for the scratch that they ask for.
+GroupArgs size_args(int experts, int64_t rows, int64_t cols, int64_t n, int cus) {
+    GroupArgs a{};
+    a.E = experts;
+    a.R = int32_t(rows);
+    a.C = int32_t(cols);
+    a.ldx = cols;
+    a.n = n;
+    a.cus = cus;
+    return a;
+}
 
 }  // namespace
 
 uint64_t linear_scratch(bool pal, int64_t rows, int64_t cols, int64_t batch, int cus) {
-    GroupArgs a{};
-    a.R = int32_t(rows);
-    a.C = int32_t(cols);
-    a.n = batch;
-    a.E = 1;
-    a.cus = cus;
-    if (rows == 0 || few_rows(a)) return 0;
-    const PalPlan p = pal ? pal_plan(a) : PLAN_TILES;
-    if (p == PLAN_SUMS) return sums_bytes(a, lds_gemm_default_split(SRC_PAL, mat_args(a), cus));
-    if (pal && p == PLAN_TILES) return 0;
-    const TilePlan t = plan_tiles(false, 1, double(a.n), true, true, a);
-    return (p == PLAN_EXPAND ? expanded_bytes(a) : 0) + (t.split > 1 ? sums_bytes(a, t.split) : 0);
+    const GroupArgs a = size_args(1, rows, cols, batch, cus);
+    if (rows == 0 || batch <= 2) return 0;
+    return choice_bytes(choose(linear_problem(pal, a), UINT64_MAX), false, a);
 }
 
 hipError_t launch_linear(bool pal, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s) {
     if (a.n <= 0 || a.R <= 0) return hipSuccess;
     if (a.n <= 2 && gemv_rows_supported(a, int(a.n))) return launch_gemv_rows(pal, false, a, int(a.n), s);
-    if (few_rows(a)) return launch_skinny_rows(pal, false, a, int(a.n), s);
-    if (!pal) return linear_tiles(a, scratch, scratch_bytes, s);
-    const PalPlan plan = pal_plan(a);
-    if (plan == PLAN_EXPAND && scratch_bytes >= expanded_bytes(a)) {
-        GroupArgs b = a;
-        const hipError_t e = expand(a, &b.w[0], static_cast<uint16_t*>(scratch), s);
-        if (e != hipSuccess) return e;
-        return linear_tiles(b, static_cast<uint8_t*>(scratch) + expanded_bytes(a), scratch_bytes - expanded_bytes(a), s);
-    }
-    if (plan == PLAN_SUMS && a.ldx == a.C) {
-        MatArgs m = mat_args(a);
-        m.split_k = lds_gemm_default_split(SRC_PAL, m, a.cus);
-        if (sums_bytes(a, m.split_k) <= scratch_bytes) {
+    const Choice c = choose(linear_problem(pal, a), scratch_bytes);
+    switch (c.kernel) {
+        case Choice::SKINNY: return launch_skinny_rows(pal, false, a, c.shape, s);
+        case Choice::TILE: return linear_tiles(a, c, scratch, s);
+        case Choice::PAL_TILE: return launch_tile_pal(false, a, PalTileShape(c.shape), s);
+        case Choice::SUMS: {
+            MatArgs m = mat_args(a);
+            m.split_k = c.split;
             m.Y = m.partial = static_cast<float*>(scratch);
             const hipError_t e = launch_lds_gemm(SRC_PAL, m, s);
-            return e == hipSuccess ? add_sums(a, m.partial, m.split_k, s) : e;
+            return e == hipSuccess ? add_sums(a, m.partial, c.split, s) : e;
+        }
+        default: {
+            GroupArgs b = a;
+            const hipError_t e = expand(a, &b.w[0], static_cast<uint16_t*>(scratch), s);
+            return e == hipSuccess ? linear_tiles(b, c, static_cast<uint8_t*>(scratch) + expanded_bytes(a), s) : e;
         }
     }
-    // 64 x 64 tiles until they take four rounds (14336 x 4096, 64 rows: 45 us
-    // against 68), then 128 x 128 (8192 x 8192 x 8192: 1.60 against 2.9 ms)
-    const int64_t units = (a.n + 63) / 64 * ((a.R + 63) / 64);
-    return launch_tile_pal(false, a, units <= 8 * int64_t(a.cus) ? PAL_TILE_64x64 : PAL_TILE_128x128, s);
 }
 
-uint64_t grouped_scratch(bool pal, bool pair, int experts, int64_t rows, int64_t cols, int64_t n) {
-    GroupArgs a{};
-    a.R = int32_t(rows);
-    a.C = int32_t(cols);
-    a.E = experts;
-    a.n = n;
-    return pal && rows && n && expand_groups(a) ? expanded_bytes(a) * (pair ? 2 : 1) : 0;
+uint64_t grouped_scratch(bool pal, bool pair, int experts, int64_t rows, int64_t cols, int64_t n, int cus) {
+    const GroupArgs a = size_args(experts, rows, cols, n, cus);
+    return pal && rows && n ? choice_bytes(choose(grouped_problem(pal, pair, a), UINT64_MAX), pair, a) : 0;
 }
 
 hipError_t launch_grouped(bool pal, bool pair, const GroupArgs& a, void* scratch, uint64_t scratch_bytes, hipStream_t s) {
     if (a.n <= 0 || a.R <= 0) return hipSuccess;
-    const int64_t groups = std::min<int64_t>(a.n, a.E);
-    const double rows = double(a.n) / double(groups);
     // one token's slots (each its own expert), or as few as to make equal ones
     // rare: the weight stream at its best; two rows for about two tokens' worth
     // of many experts (gate/up of 4 tokens, 16 experts: 34 us against 37-40)
     const bool single = a.order ? a.n <= a.div : 4 * a.n <= a.E || a.n == 1;
     if (single && gemv_rows_supported(a, 1)) return launch_gemv_rows(pal, pair, a, 1, s);
     if (2 * a.n <= a.E && gemv_rows_supported(a, 2)) return launch_gemv_rows(pal, pair, a, 2, s);
-    // gate/up of 16 experts, 2 rows each: 4-row tiles 68 (bf16) and 74 us
-    // (palette), 16-row ones 79 and 67; 4 rows each: 16-row ones 79 against 86;
-    // 12 rows of 32 experts: 16-row ones 62 (bf16), 72 us (palette, 63 with tiles)
-    if (rows <= (pal ? 1.5 : 2.5)) return launch_skinny_rows(pal, pair, a, 4, s);
-    if (rows <= (pal ? 11 : 14)) return launch_skinny_rows(pal, pair, a, 16, s);
-    if (!pal) return launch_tile(pair, a, plan_tiles(pair, double(groups), rows, false, false, a).shape, s);
-    if (expand_groups(a) && scratch_bytes >= expanded_bytes(a) * (pair ? 2 : 1)) {
-        GroupArgs b = a;
-        for (int m = 0; m < (pair ? 2 : 1); ++m) {
-            const hipError_t e = expand(a, &b.w[m], static_cast<uint16_t*>(scratch) + uint64_t(m) * (expanded_bytes(a) / 2), s);
-            if (e != hipSuccess) return e;
+    const Choice c = choose(grouped_problem(pal, pair, a), scratch_bytes);
+    switch (c.kernel) {
+        case Choice::SKINNY: return launch_skinny_rows(pal, pair, a, c.shape, s);
+        case Choice::PAL_TILE: return launch_tile_pal(pair, a, PalTileShape(c.shape), s);
+        case Choice::TILE: return launch_tile(pair, a, TileShape(c.shape), s);
+        default: {                                       // expanded
+            GroupArgs b = a;
+            for (int m = 0; m < (pair ? 2 : 1); ++m) {
+                uint16_t* const out = static_cast<uint16_t*>(scratch) + uint64_t(m) * (expanded_bytes(a) / 2);
+                const hipError_t e = expand(a, &b.w[m], out, s);
+                if (e != hipSuccess) return e;
+            }
+            return launch_tile(pair, b, TileShape(c.shape), s);
         }
-        return launch_tile(pair, b, plan_tiles(pair, double(groups), rows, false, false, b).shape, s);
     }
-    // 25 rows of 8 experts: 128 x 64 tiles 111 us, 128 x 128 123; 64 rows: 151
-    // and 122
-    return launch_tile_pal(pair, a, rows <= 40 ? PAL_TILE_128x64 : PAL_TILE_128x128, s);
 }
 
 }  // namespace uwk

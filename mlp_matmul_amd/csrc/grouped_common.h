@@ -116,22 +116,56 @@ __device__ __forceinline__ const uint16_t* group_x_row(const GroupArgs& a, int64
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
+// x / (1 + exp(-x)) from the hardware's base-2 exponential and reciprocal, each
+// within one unit in the last place: a rounding of -x log2(e) is worth |x| 2^-24
+// of exp(-x), which counts where exp(-x) is not small against 1 and |x| is.
+__device__ __forceinline__ float silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case ACT_RELU: return v < 0.f ? 0.f : v;           // NaN stays
-        case ACT_SILU: return v / (1.0f + expf(-v));
+        case ACT_SILU: return silu(v);
         case ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-        case ACT_GELU_TANH: return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * fmaf(0.044715f * v * v, v, v)));
+        // 1 + tanh(u) = 2 / (1 + exp(-2u))
+        case ACT_GELU_TANH:
+            return v * __builtin_amdgcn_rcpf(
+                1.0f + __builtin_amdgcn_exp2f(-2.0f * 1.4426950408889634f * 0.79788456080286536f * fmaf(0.044715f * v * v, v, v)));
         default: return v;
     }
 }
 
-// Four values of rows r .. r+3 from p[r..], of either type; those from R on are 0.
-__device__ __forceinline__ f32x4_t load4(const void* p, int type, int64_t o, int r, int R, bool aligned) {
+// The same for 4 N values, the choice made once.
+template <int N>
+__device__ __forceinline__ void activate_all(f32x4_t (&v)[N], int act) {
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[k][j] = f(v[k][j]);
+    };
+    switch (act) {
+        case ACT_RELU: each([](float x) { return activate(x, ACT_RELU); }); break;
+        case ACT_SILU: each([](float x) { return activate(x, ACT_SILU); }); break;
+        case ACT_GELU: each([](float x) { return activate(x, ACT_GELU); }); break;
+        case ACT_GELU_TANH: each([](float x) { return activate(x, ACT_GELU_TANH); }); break;
+        default: break;
+    }
+}
+
+// Four elements that need not be aligned to four: the hardware takes any
+// multiple of the element.
+typedef uint32_t u32x2_e2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// Four values of rows r .. r+3 from p[o..], of either type; those from R on are 0.
+__device__ __forceinline__ f32x4_t load4(const void* p, int type, int64_t o, int r, int R) {
     f32x4_t v{0.f, 0.f, 0.f, 0.f};
-    if (aligned && r + 3 < R) {
-        if (type == VT_F32) return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + o);
-        const u32x2_t q = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + o);
+    if (r + 3 < R) {
+        if (type == VT_F32)
+            return __builtin_bit_cast(f32x4_t, u32x4_t(*reinterpret_cast<const u32x4_e4_t*>(static_cast<const float*>(p) + o)));
+        const u32x2_t q = *reinterpret_cast<const u32x2_e2_t*>(static_cast<const uint16_t*>(p) + o);
         return f32x4_t{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xFFFF0000u), __uint_as_float(q[1] << 16),
                        __uint_as_float(q[1] & 0xFFFF0000u)};
     }
@@ -142,6 +176,32 @@ __device__ __forceinline__ f32x4_t load4(const void* p, int type, int64_t o, int
     return v;
 }
 
+// Four values to rows r .. r+3, those below R.
+__device__ __forceinline__ void store4(void* p, int type, int64_t o, int r, int R, f32x4_t v) {
+    if (type == VT_BF16) {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_rne(v[i]);
+        uint16_t* const d = static_cast<uint16_t*>(p) + o;
+        if (r + 3 < R) {
+            *reinterpret_cast<u32x2_e2_t*>(d) = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r + i < R) d[i] = uint16_t(h[i]);
+        }
+    } else {
+        float* const d = static_cast<float*>(p) + o;
+        if (r + 3 < R) {
+            *reinterpret_cast<u32x4_e4_t*>(d) = __builtin_bit_cast(u32x4_t, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r + i < R) d[i] = v[i];
+        }
+    }
+}
+
 // What the epilogue of weight rows r .. r+3 (those below R) and output row b
 // reads.
 struct EpilogueIn {
@@ -150,46 +210,102 @@ struct EpilogueIn {
 
 __device__ __forceinline__ EpilogueIn epilogue_load(const Epilogue& ep, int64_t b, int r, int R) {
     EpilogueIn in{};
-    if (ep.bias) in.bias = load4(ep.bias, ep.bias_type, r, r, R, true);
-    if (ep.residual) in.residual = load4(ep.residual, ep.residual_type, b * ep.ldr + r, r, R, (ep.ldr & 3) == 0);
+    if (ep.bias) in.bias = load4(ep.bias, ep.bias_type, r, r, R);
+    if (ep.residual) in.residual = load4(ep.residual, ep.residual_type, b * ep.ldr + r, r, R);
     return in;
 }
 
-// Bias, activation, residual, and the one rounding to the output's type;
-// vector stores where rows are 4-element aligned.
+// Bias, activation, residual, and the one rounding to the output's type.
 __device__ __forceinline__ void epilogue_store(const Epilogue& ep, const EpilogueIn& in, int64_t b, int r, int R,
                                                f32x4_t v) {
-    const bool whole = r + 3 < R && (ep.ldo & 3) == 0;
     if (ep.bias) v += in.bias;
     if (ep.act != ACT_NONE) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = activate(v[i], ep.act);
     }
     if (ep.residual) v += in.residual;
-    const int64_t o = b * ep.ldo + r;
-    if (ep.out_type == VT_BF16) {
-        uint32_t h[4];
+    store4(ep.out, ep.out_type, b * ep.ldo + r, r, R, v);
+}
+
+// The epilogue of a tile from LDS, in parts of `kIn` input rows by `kRows`
+// weight rows (floats at part[n * ES + r]) that `kThreads` threads share, four
+// elements of a row a lane.  A lane's weight rows are the same in every item and
+// part, so that its bias is loaded once, and residuals of the next part are on
+// their way while this one is stored.
+template <int kRows, int kIn, int kThreads, int ES>
+struct PartEpilogue {
+    static constexpr int kItems = kRows * kIn / 4 / kThreads;
+    static_assert(kItems >= 1 && kItems * 4 * kThreads == kRows * kIn && kThreads % (kRows / 4) == 0, "whole items");
+    const Epilogue& ep;
+    const float* const part;
+    const int64_t first;                                     // the tile's first output row
+    const int rows, r, R, tid;                               // its output rows, the lane's first weight row
+    f32x4_t bias;
+    u32x4_t res[kItems];                                     // as loaded: a conversion would wait for them
+
+    __device__ __forceinline__ PartEpilogue(const Epilogue& e, const float* p, const GroupTile& t, uint32_t row0, int R_,
+                                            int tid_)
+        : ep(e), part(p), first(t.row0), rows(t.rows), r(int(row0) + tid_ % (kRows / 4) * 4), R(R_), tid(tid_),
+          bias{0.f, 0.f, 0.f, 0.f} {
+        if (ep.bias) bias = load4(ep.bias, ep.bias_type, r, r, R);
+    }
+    __device__ __forceinline__ int input_row(int k) const { return (tid + k * kThreads) / (kRows / 4); }
+    __device__ __forceinline__ f32x4_t value(int k) const {
+        return *reinterpret_cast<const f32x4_t*>(part + input_row(k) * ES + tid % (kRows / 4) * 4);
+    }
+
+    // row(n): input row n of the part in the tile
+    template <class Row>
+    __device__ __forceinline__ void load(Row&& row) {
+        if (!ep.residual || r + 3 >= R) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16_rne(v[i]);
-        uint16_t* p = static_cast<uint16_t*>(ep.out) + o;
-        if (whole) {
-            *reinterpret_cast<u32x2_t*>(p) = u32x2_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (r + i < R) p[i] = uint16_t(h[i]);
-        }
-    } else {
-        float* p = static_cast<float*>(ep.out) + o;
-        if (whole) {
-            *reinterpret_cast<f32x4_t*>(p) = v;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (r + i < R) p[i] = v[i];
+        for (int k = 0; k < kItems; ++k) {
+            const int b = row(input_row(k));
+            const int64_t o = (first + b) * ep.ldr + r;
+            if (b >= rows) continue;
+            if (ep.residual_type == VT_F32) {
+                res[k] = *reinterpret_cast<const u32x4_e4_t*>(static_cast<const float*>(ep.residual) + o);
+            } else {
+                const u32x2_t h = *reinterpret_cast<const u32x2_e2_t*>(static_cast<const uint16_t*>(ep.residual) + o);
+                res[k] = u32x4_t{h[0], h[1], 0u, 0u};
+            }
         }
     }
-}
+    // stores the part with the residuals that were loaded for it, and loads the
+    // next one's: row of this part, next of the next
+    template <class Row, class Next>
+    __device__ __forceinline__ void store(Row&& row, bool more, Next&& next) {
+        if (r + 3 >= R) return store_last(row);
+        f32x4_t v[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) v[k] = value(k) + bias;
+        activate_all(v, ep.act);
+        if (ep.residual) {
+#pragma unroll
+            for (int k = 0; k < kItems; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[k][j] += __uint_as_float(ep.residual_type == VT_F32 ? res[k][j]
+                                               : j & 1                    ? res[k][j >> 1] & 0xFFFF0000u
+                                                                          : res[k][j >> 1] << 16);
+        }
+        if (more) load(next);
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int b = row(input_row(k));
+            if (b < rows) store4(ep.out, ep.out_type, (first + b) * ep.ldo + r, r, R, v[k]);
+        }
+    }
+    // the lanes of the last weight rows, fewer than four
+    template <class Row>
+    __device__ __forceinline__ void store_last(Row&& row) {
+#pragma unroll 1
+        for (int k = 0; k < kItems; ++k) {
+            const int b = row(input_row(k));
+            if (b < rows && r < R) epilogue_store(ep, epilogue_load(ep, first + b, r, R), first + b, r, R, value(k));
+        }
+    }
+};
 
 __device__ __forceinline__ void epilogue4(const Epilogue& ep, int64_t b, int r, int R, f32x4_t v) {
     epilogue_store(ep, epilogue_load(ep, b, r, R), b, r, R, v);

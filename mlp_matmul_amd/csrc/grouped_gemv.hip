@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a,
                     gate[b] = v;
                     continue;
                 }
-                v = silu_mul1(gate[b], v);
+                v = silu(gate[b]) * v;
             }
             if (lane == 0 && b < t.rows && p.row < my_rows) {
                 if (a.ep.bias) v += bias;

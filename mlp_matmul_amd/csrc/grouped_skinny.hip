@@ -23,6 +23,8 @@
 //   Measured: gate/up of 33 tokens, 16 experts of 1792 x 4096 in bf16, 83 us for
 // 470 MB (5.7 TB/s); 16 rows of 4096 x 14336, palette, 24 us for 91 MB, 8 of
 // them the launch, the first loads and the last sums.
+#include <algorithm>
+
 #include "grouped_common.h"
 #include "kernels.h"
 
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(GroupArgs a, uint32_t b
         if (b >= uint32_t(t.rows) || row >= R) continue;
         if (PAIR) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = silu_mul1(y[c], u[c]);
+            for (int c = 0; c < 4; ++c) y[c] = silu(y[c]) * u[c];
         }
         if (i != wave) in = epilogue_load(a.ep, t.row0 + b, int(row), a.R);
         epilogue_store(a.ep, in, t.row0 + b, int(row), a.R, y);
@@ -385,18 +387,14 @@ hipError_t launch_kw(const GroupArgs& a, int64_t bands, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Waves that split K: the fewest (2, 4 or 8) that give about six waves a
-// compute unit; more only add to the partial sums and to what starts and ends
-// together (16 rows of 14336 x 4096, palette: 22.7 us with two, 25.8 with four;
-// of 4096 x 14336: 36.2, 23.6, 23.4 with two, four, eight).  The rings of eight
-// fit a compute unit's LDS through 16 input rows of a single matrix.
 template <bool PAL, bool PAIR, int XQ>
 hipError_t launch(const GroupArgs& a, hipStream_t s) {
-    const int64_t bands = (a.R + 15) / 16, active = a.offsets ? (a.n < a.E ? a.n : a.E) : 1;
-    const int64_t most = active > 1 ? active : 1, want = 6 * int64_t(a.cus);
-    if (2 * bands * most >= want) return launch_kw<PAL, PAIR, XQ, 2>(a, bands, s);
-    if (PAIR || XQ > 4 || 4 * bands * most >= want) return launch_kw<PAL, PAIR, XQ, 4>(a, bands, s);
-    return launch_kw<PAL, PAIR, XQ, (PAIR || XQ > 4 ? 4 : 8)>(a, bands, s);
+    const int64_t bands = (a.R + 15) / 16;
+    switch (skinny_waves(PAIR, 4 * XQ, a)) {
+        case 2: return launch_kw<PAL, PAIR, XQ, 2>(a, bands, s);
+        case 4: return launch_kw<PAL, PAIR, XQ, 4>(a, bands, s);
+        default: return launch_kw<PAL, PAIR, XQ, (PAIR || XQ > 4 ? 4 : 8)>(a, bands, s);
+    }
 }
 
 template <bool PAL, bool PAIR>
@@ -406,6 +404,17 @@ hipError_t launch_xq(const GroupArgs& a, int rows, hipStream_t s) {
 }
 
 }  // namespace
+
+// Waves that split K: the fewest (2, 4 or 8) that give about six waves a
+// compute unit; more only add to the partial sums and to what starts and ends
+// together (16 rows of 14336 x 4096, palette: 22.7 us with two, 25.8 with four;
+// of 4096 x 14336: 36.2, 23.6, 23.4 with two, four, eight).  The rings of eight
+// fit a compute unit's LDS through 16 input rows of a single matrix.
+int skinny_waves(bool pair, int rows, const GroupArgs& a) {
+    const int64_t bands = (a.R + 15) / 16, most = std::max<int64_t>(a.offsets || a.E > 1 ? std::min<int64_t>(a.n, a.E) : 1, 1);
+    const int64_t want = 6 * int64_t(a.cus);
+    return 2 * bands * most >= want ? 2 : pair || rows > 16 || 4 * bands * most >= want ? 4 : 8;
+}
 
 hipError_t launch_skinny_rows(bool pal, bool pair, const GroupArgs& a, int rows, hipStream_t s) {
     if (pal) return pair ? launch_xq<true, true>(a, rows, s) : launch_xq<true, false>(a, rows, s);

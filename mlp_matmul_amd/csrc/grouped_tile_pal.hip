@@ -239,6 +239,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void tile_pal_kernel(GroupArgs a, 
     __builtin_amdgcn_s_waitcnt(0);
 
     constexpr int OM = PAIR ? FM / 2 : FM;
+    PartEpilogue<kRows, 16 * EC, 64 * NW, ES> out(a.ep, part, t, row0, a.R, tid);
+    auto rows_of = [](int p) { return [p](int n) { return ((p / FN * EC + n / 16) * FN + p % FN) * 16 + n % 16; }; };
+    out.load(rows_of(0));
 #pragma unroll 1
     for (int p = 0; p < FN * (WN / EC); ++p) {
         __syncthreads();
@@ -251,19 +254,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void tile_pal_kernel(GroupArgs a, 
                 f32x4_t v = acc[i][j];
                 if (PAIR) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = silu_mul1(v[c], acc[FM - OM + i][j][c]);
+                    for (int c = 0; c < 4; ++c) v[c] = silu(v[c]) * acc[FM - OM + i][j][c];
                 }
                 *reinterpret_cast<f32x4_t*>(part + ((wn - c0) * 16 + int(rl)) * ES + (wm * OM + i) * 16 + 4 * int(q)) = v;
             }
         }
         __syncthreads();
-#pragma unroll 1
-        for (int i = tid; i < EC * 16 * (kRows / 4); i += 64 * NW) {
-            const int n = i / (kRows / 4), r = i % (kRows / 4) * 4;
-            const int b = ((c0 + n / 16) * FN + p % FN) * 16 + n % 16;
-            if (b < t.rows && row0 + uint32_t(r) < R)
-                epilogue4(a.ep, t.row0 + b, int(row0) + r, a.R, *reinterpret_cast<const f32x4_t*>(part + n * ES + r));
-        }
+        out.store(rows_of(p), p + 1 < FN * (WN / EC), rows_of(p + 1));
     }
 }
 

@@ -313,12 +313,11 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     if (i >= a.tokens * quads) return;
     const int64_t t = i / quads;
     const int c = int(i % quads) * 4, C = int(a.cols);
-    const bool aligned = (C & 3) == 0;
     f32x4_t v{0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < a.top_k; ++j) {
         const int32_t p = a.place[t * a.top_k + j];
         if (p < 0 || p >= a.n) continue;
-        const f32x4_t y = load4(a.Y, VT_F32, int64_t(p) * C + c, c, C, aligned);
+        const f32x4_t y = load4(a.Y, VT_F32, int64_t(p) * C + c, c, C);
         const float w = a.weights[t * a.top_k + j];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = fmaf(w, y[k], v[k]);

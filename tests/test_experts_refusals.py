@@ -141,22 +141,23 @@ def test_scratch_sizes():
     assert L.uw_moe_scratch_bytes(0, 3, 8, 2, 64, 128) == 256 * 5 + 6 * 64 * 2 + 6 * 128 * 4
     assert L.uw_moe_scratch_bytes(0, 3, 8, 2, 60, 128) == _capi.UW_EINVAL
     assert L.uw_moe_scratch_bytes(1, 3, 8, 2, 64, 128) == L.uw_moe_scratch_bytes(0, 3, 8, 2, 64, 128)
-    assert (L.uw_moe_scratch_bytes(1, 1100, 2, 1, 64, 128) ==
-            L.uw_moe_scratch_bytes(0, 1100, 2, 1, 64, 128) + 2 * 2 * 64 * 128 * 2)
-    assert L.uw_grouped_scratch_bytes(1, 1, 4, 64, 128, 512 * 4) == 0
-    assert L.uw_grouped_scratch_bytes(1, 1, 4, 64, 128, 512 * 4 + 1) == 2 * 4 * 64 * 128 * 2
+    assert (L.uw_moe_scratch_bytes(1, 9000, 2, 1, 1024, 2048) ==
+            L.uw_moe_scratch_bytes(0, 9000, 2, 1, 1024, 2048) + 2 * 2 * 1024 * 2048 * 2)
+    assert L.uw_grouped_scratch_bytes(1, 1, 4, 1024, 2048, 20 * 4) == 0
+    assert L.uw_grouped_scratch_bytes(1, 1, 4, 1024, 2048, 5000 * 4) == 2 * 4 * 1024 * 2048 * 2
+    assert L.uw_grouped_scratch_bytes(1, 0, 4, 1024, 2048, 5000 * 4) == 4 * 1024 * 2048 * 2
+    assert L.uw_grouped_scratch_bytes(0, 1, 4, 1024, 2048, 5000 * 4) == 0
     assert L.uw_grouped_scratch_bytes(1, 0, 0, 64, 128, 5) == _capi.UW_EINVAL
     assert L.uw_grouped_scratch_bytes(1, 0, 4, 64, 100, 5) == _capi.UW_EINVAL
     assert L.uw_grouped_scratch_bytes(1, 0, 4, 1 << 20, 1 << 11, 5) == _capi.UW_EUNSUPPORTED
     assert L.uw_linear_scratch_bytes(1, 64, 100, 4) == _capi.UW_EINVAL
     assert L.uw_linear_scratch_bytes(1, 1 << 20, 1 << 11, 4) == _capi.UW_EUNSUPPORTED
-    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 32) == 0
-    assert L.uw_linear_scratch_bytes(0, 4096, 4096, 16) == 0
+    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 2) == 0
+    assert L.uw_linear_scratch_bytes(0, 4096, 4096, 2) == 0
     assert L.uw_linear_scratch_bytes(0, 8192, 8192, 8192) == 0
     assert L.uw_linear_scratch_bytes(1, 8192, 8192, 8192) == 2 * 8192 * 8192
     assert L.uw_linear_scratch_bytes(0, 4096, 14336, 64) % (64 * 4096 * 4) == 0
     assert L.uw_linear_scratch_bytes(0, 4096, 14336, 64) > 0
-    assert L.uw_linear_scratch_bytes(1, 4096, 4096, 100) % (100 * 4096 * 4) == 0
 
 
 def test_scratch_refusals():

@@ -393,11 +393,11 @@ def test_grouped_verbatim_in_the_first_expert_only(torch_cuda):
 def test_grouped_scratch(torch_cuda):
     """Experts with hundreds of rows: any scratch gives the result, an expert without rows is not expanded."""
     torch = torch_cuda
-    counts, rows, cols = [900, 0, 600, 701], 130, 320
+    counts, rows, cols = [2900, 0, 1600, 2701], 1020, 1088
     (W, w), (U, u) = (make_weight(torch, 50 + i, 4, rows, cols, True, 0.02) for i in range(2))
     off, order, n = grouping(torch, 8, counts, 2, 1000)
     X = rows_of(torch, 5, 1000, cols, 8)
-    at = torch.cat([torch.arange(0, n, 17), off[1:].cpu().long() - 1])
+    at = torch.cat([torch.arange(0, n, 211), off[1:].cpu().long() - 1])
     e = torch.from_numpy(np.repeat(np.arange(4), counts))[at]
     x = f64(X)[order.cpu().long()[at] // 2]
     v, q = [torch.bmm(m[e], x[:, :, None])[:, :, 0] for m in (w, u)]
