@@ -277,8 +277,9 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a,
 //   out[r] = sum_j weights[j] * (D_e(j)[r] . h[place[j]]) (+ residual[r])
 // A wave owns an output row and walks that row of every chosen expert's matrix
 // in turn, so the sum stays in its registers: no array of the experts' outputs
-// and no launch that adds it.  Items, ring and rebuild as above; lane j*tiles +
-// i keeps the verbatim word and base of tile i of expert j's row.
+// and no launch that adds it (a layer of one token, two of 8 experts of 3584 x
+// 4096, palette: 35.5 us, 38.1 with a launch for each).  Items, ring and rebuild
+// as above; lane j*tiles + i keeps the verbatim word and base of tile i of expert j's row.
 template <bool PAL, int D>
 __global__ __launch_bounds__(64 * kGemvWaves) void gemv_combine_kernel(GroupArgs a, CombineArgs c) {
     __shared__ uint32_t lut[PAL ? 256 : 1];

@@ -21,6 +21,10 @@
 // or earlier chunks of its wave (equal experts matched bit by bit with
 // ballots).  Up to 64 tokens take one launch of one workgroup; more take a
 // launch for the selection and the blocks' counts, and one for the places.
+//
+// Measured: 8 tokens of 64 experts 4.1 us, a launch; 16384 of 256 12 us for the
+// selection, bound by vector instructions (85 a round of four tokens), and 8 for the
+// places, bound by the latency of a chain of small steps.
 #include <float.h>
 
 #include <algorithm>
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
 }
 
 // out[t] = sum_j weights[t][j] * Y[place[t][j]] (+ residual[t]), j ascending.
-// Memory bound: four columns a lane.
+// Memory bound: four columns a lane (600 tokens of 4 experts, 2048 columns: 6.9 us).
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     const int64_t quads = (a.cols + 3) / 4, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (i >= a.tokens * quads) return;

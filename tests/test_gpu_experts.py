@@ -390,6 +390,47 @@ def test_grouped_verbatim_in_the_first_expert_only(torch_cuda):
                   torch.stack([(cols + 8) * 2.0 ** -23 * (hx[j].abs() @ exact[e[j]].abs().t()) for j in range(2)]), "routed")
 
 
+@pytest.mark.parametrize("pal", [False, True])
+def test_grouped_past_32_bits(torch_cuda, pal):
+    """The last expert of a stack of more than 2^31 weights gives what its own matrix gives.  The bound on either
+    sum is that of fp32 sums, with the sum of absolute products from the same matrix without its signs."""
+    torch = torch_cuda
+    E, R, C = 36, 8192, 8192
+    one, tiles = R * C, R * C // 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    if pal:
+        sm = torch.randint(0, 256, (E * one,), generator=g, dtype=torch.uint8, device="cuda")
+        nib = torch.randint(0, 256, (E * one // 2,), generator=g, dtype=torch.uint8, device="cuda")
+        vexp = torch.randint(108, 122, (E * tiles * 64,), generator=g, dtype=torch.uint8, device="cuda")
+
+        def handle(lo, hi, mask=255):                        # the first group of every tile is verbatim
+            n = (hi - lo) * tiles
+            return uw.DeviceMatrix.from_sections((hi - lo) * R, C, range(106, 122), n, {
+                "sm": sm[lo * one:hi * one] if mask == 255 else sm[lo * one:hi * one] & mask,
+                "nib": nib[lo * one // 2:hi * one // 2], "vexp": vexp[lo * tiles * 64:hi * tiles * 64],
+                "bitmap": torch.ones(n, dtype=torch.int64, device="cuda").view(torch.uint8),
+                "tile_vbase": torch.arange(n + 1, dtype=torch.int32, device="cuda").view(torch.uint8)})
+        whole, last, size = handle(0, E), handle(E - 1, E), handle(E - 1, E, 0x7F)
+    else:
+        whole = torch.empty(E, R, C, dtype=torch.bfloat16, device="cuda")
+        for e in range(E):
+            whole[e] = torch.randn(R, C, generator=g, device="cuda") * 0.02
+        last, size = whole[E - 1], whole[E - 1].abs()
+    for n in (1, 3, 40, 700):
+        print_case(f"last of {E} experts, {n} rows, pal={pal}")
+        X = rows_of(torch, n, n, C)
+        off = torch.zeros(E + 1, dtype=torch.int32).cuda()
+        off[E] = n
+        bound = 2 * (C + 8) * 2.0 ** -23 * f64(uw.linear(size, X.abs())) * 1.01
+        want = uw.linear(last, X)
+        assert bool(want.isfinite().all())
+        check(torch, uw.gemm_grouped(whole, X, off), f64(want), bound, "products")
+        h, q = uw.moe_gate_up(whole, whole, X, off), f64(want)
+        y = activate(torch, q, "silu")
+        check(torch, h, y * q, (1.13 * bound + 2.0 ** -20 * (q.abs() + y.abs())) * (q.abs() + bound) + y.abs() * bound +
+              (y * q).abs() * 2.0 ** -23, "pair")
+
+
 def test_grouped_scratch(torch_cuda):
     """Experts with hundreds of rows: any scratch gives the result, an expert without rows is not expanded."""
     torch = torch_cuda
