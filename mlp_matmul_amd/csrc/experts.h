@@ -95,7 +95,7 @@ struct RouteArgs {
     int32_t* order;
     int32_t* place;
     uint16_t* counts;           // [blocks, experts up to 8s] of every block's slots, when blocks > 1
-    int32_t blocks, per_block;  // tokens of a block: a multiple of 64
+    int32_t blocks, per_block;  // tokens of a block: a multiple of 16
 };
 
 // Blocks of tokens of a routing call (1: a single launch, no counts).

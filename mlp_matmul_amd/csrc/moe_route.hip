@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kRT = 1024;            // threads of a workgroup
 constexpr int kRW = kRT / 64;        // its waves
-constexpr int kMaxBlocks = 256;      // one a compute unit (16384 tokens in blocks of 64), until 16 bits end
+constexpr int kMaxBlocks = 256;      // one a compute unit (16 to 64 tokens each through 16384), until 16 bits end
 
 template <int N>
 __device__ __forceinline__ uint32_t row_ror(uint32_t v) {
@@ -174,7 +174,8 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     const uint32_t lane = uint32_t(tid) & 63u, sub = lane & 15u;
     const int E = a.experts, K = a.top_k, vecs = (E + 7) / 8;
     const int64_t tb = int64_t(blockIdx.x) * a.per_block;  // the block's tokens, the wave's inside them
-    const int64_t t_lo = tb + int64_t(wave) * (a.per_block / kRW), t_hi = min(t_lo + a.per_block / kRW, a.tokens);
+    const int waves = PHASE == 1 ? int(blockDim.x >> 6) : kRW;
+    const int64_t t_lo = tb + int64_t(wave) * (a.per_block / waves), t_hi = min(t_lo + a.per_block / waves, a.tokens);
     auto slot_id = [&](int64_t i) { return i < t_hi * K ? a.ids[i] : -1; };
 
     const int groups = min(kRT / vecs, 32), g = tid / vecs;                // of blocks; this thread's
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
             if (lo + i < hi) q[i] = counts[int64_t(lo + i) * vecs];
     }
     if (PHASE == 1) {
-        for (int e = tid; e < vecs * 8; e += kRT) cnt[0][e] = 0;
+        for (int e = tid; e < vecs * 8; e += int(blockDim.x)) cnt[0][e] = 0;
     } else {
         for (int e = int(lane); e < E; e += 64) cnt[wave][e] = 0;
     }
@@ -332,8 +333,9 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 }  // namespace
 
 void route_blocks(int64_t tokens, int32_t* blocks, int32_t* per_block) {
-    const int64_t per = ((tokens + kMaxBlocks - 1) / kMaxBlocks + 63) / 64 * 64;
-    *per_block = int32_t(std::min<int64_t>(std::max<int64_t>(per, 64), 65472));   // counts fit 16 bits
+    const int64_t unit = tokens <= 64 || tokens > 64 * kMaxBlocks ? 64 : 16;
+    const int64_t per = ((tokens + kMaxBlocks - 1) / kMaxBlocks + unit - 1) / unit * unit;
+    *per_block = int32_t(std::min<int64_t>(std::max<int64_t>(per, unit), 65472));   // counts fit 16 bits
     const int64_t n = (tokens + *per_block - 1) / *per_block;
     *blocks = int32_t(n > 1 ? n : 1);                      // no tokens: one block writes the offsets
 }
@@ -345,7 +347,8 @@ hipError_t launch(const RouteArgs& a, hipStream_t s) {
         route_kernel<0, V><<<1, kRT, 0, s>>>(a);
         return hipGetLastError();
     }
-    route_kernel<1, V><<<unsigned(a.blocks), kRT, 0, s>>>(a);
+    // four tokens a wave at a time, as many waves as the block's tokens keep busy
+    route_kernel<1, V><<<unsigned(a.blocks), unsigned(std::min(kRT, a.per_block * 16)), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     route_kernel<2, 1><<<unsigned(a.blocks), kRT, 0, s>>>(a);

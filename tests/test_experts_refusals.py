@@ -135,7 +135,7 @@ def test_compressed_weights():
 def test_scratch_sizes():
     L = uw.lib()
     assert L.uw_moe_route_scratch_bytes(64, 256, 8) == 0
-    assert L.uw_moe_route_scratch_bytes(65, 256, 8) == 2 * 256 * 2
+    assert L.uw_moe_route_scratch_bytes(65, 256, 8) == 5 * 256 * 2
     assert L.uw_moe_route_scratch_bytes(1 << 24, 16, 8) == 8448          # 257 blocks of 32 bytes, up to 256
     assert L.uw_moe_route_scratch_bytes(1, 0, 1) == _capi.UW_EINVAL
     assert L.uw_moe_scratch_bytes(0, 3, 8, 2, 64, 128) == 256 * 5 + 6 * 64 * 2 + 6 * 128 * 4

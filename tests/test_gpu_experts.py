@@ -245,7 +245,7 @@ def check_route(torch, logits, top_k, renorm, what):
     return got
 
 
-@pytest.mark.parametrize("tokens", [0, 1, 3, 63, 64, 65, 200, 1000, 9001])
+@pytest.mark.parametrize("tokens", [0, 1, 3, 63, 64, 65, 200, 1000, 4100, 9001, 16390])
 def test_route(torch_cuda, tokens):
     torch = torch_cuda
     g = torch.Generator().manual_seed(tokens)
@@ -254,6 +254,28 @@ def test_route(torch_cuda, tokens):
         l = torch.randn(tokens, experts, generator=g)
         check_route(torch, l.cuda(), top_k, True, f"route {tokens} of {experts} top {top_k}")
         check_route(torch, l.bfloat16().cuda(), top_k, False, f"route bf16 {tokens} of {experts} top {top_k}")
+
+
+def test_route_many_tokens(torch_cuda):
+    """More tokens than fit 256 blocks whose counts have 16 bits; a padded one among them."""
+    torch = torch_cuda
+    tokens = (1 << 24) + 777
+    print_case(f"route {tokens} tokens")
+    l = torch.randn(tokens, 2, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    l[tokens // 2] = -math.inf
+    l[:70000, 1] = -100.0                                    # a block's tokens all on one expert
+    r = uw.moe_route(l, 1)
+    ids = torch.where(l[:, 1] > l[:, 0], 1, 0)
+    ids[tokens // 2] = 2
+    order = torch.sort(ids, stable=True).indices
+    n0, n1 = int((ids == 0).sum()), int((ids == 1).sum())
+    assert r.offsets.tolist() == [0, n0, n0 + n1] and n0 + n1 == tokens - 1
+    assert torch.equal(r.ids[:, 0], torch.where(ids == 2, -1, ids).int())
+    order[-1] = -1
+    assert torch.equal(r.order, order.int())
+    place = torch.full((tokens,), -1, dtype=torch.int32, device="cuda")
+    place[order[:-1]] = torch.arange(tokens - 1, dtype=torch.int32, device="cuda")
+    assert torch.equal(r.place[:, 0], place)
 
 
 def test_route_ties_masks_and_strides(torch_cuda):
