@@ -434,6 +434,19 @@ def _elsewhere(dev, stream):
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev))
 
 
+def _new_scratch(need, least, dev):
+    """`need` bytes, or where memory has no room for them the `least` that the
+    call runs with (None: none)."""
+    torch = _torch()
+    if need > 0:
+        try:
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        except torch.cuda.OutOfMemoryError:
+            if need == least:
+                raise
+    return torch.empty(least, dtype=torch.uint8, device=dev) if least else None
+
+
 def _scratch_arg(scratch):
     """(its pointer, its bytes)"""
     if scratch is None:
@@ -482,8 +495,7 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     out, ldo, out_type = _out_arg(out, batch, rows, out_dtype, dev)
     if scratch is None and batch > 2:                        # never any through 2 rows
         need = lib().uw_linear_scratch_bytes(0 if d is None else 1, rows, cols, batch)
-        if need > 0:
-            scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        scratch = _new_scratch(need, 0, dev)
     sp, sb = _scratch_arg(scratch)
     check(lib().uw_linear(w, d, rows, cols, X.data_ptr(), ldx, batch, None if bias is None else bias.data_ptr(),
                           UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type, ldr,
@@ -532,12 +544,11 @@ def _group_args(X, offsets, order):
 
 def _grouped_scratch(scratch, d, pair, experts, rows, cols, n, dev):
     """(the tensor, its pointer, its bytes)"""
-    if scratch is None and d is not None and n > 64:         # it may help some rows later
+    if scratch is None and d is not None and n > 64:         # below, none is taken
         need = lib().uw_grouped_scratch_bytes(1, pair, experts, rows, cols, n)
         if need < 0:
             check(int(need), "uw_grouped_scratch_bytes")
-        if need:
-            scratch = _torch().empty(need, dtype=_torch().uint8, device=dev)
+        scratch = _new_scratch(need, 0, dev)
     return (scratch, *_scratch_arg(scratch))
 
 
@@ -627,7 +638,6 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     if ctx is not None:
         with ctx:
             return moe_layer(gate, up, down, X, logits, top_k, renormalize, residual, out, out_dtype, scratch)
-    torch = _torch()
     tokens, experts = X.shape[0], logits.shape[-1]
     ldl, kind = _matrix_arg(logits, "logits", tokens), _value_type(logits, "logits")
     gw, gd, F, H = _weight_arg(gate, experts, "gate")
@@ -639,7 +649,9 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     res, res_type, ldr = _residual_arg(residual, tokens, H)
     out, ldo, out_type = _out_arg(out, tokens, H, out_dtype, dev)
     if scratch is None:
-        scratch = torch.empty(moe_scratch_bytes(tokens, experts, top_k, F, H, bool(gd or dd)), dtype=torch.uint8, device=dev)
+        least = moe_scratch_bytes(tokens, experts, top_k, F, H)
+        need = moe_scratch_bytes(tokens, experts, top_k, F, H, True) if gd or dd else least
+        scratch = _new_scratch(need, least, dev)
     sp, sb = _scratch_arg(scratch)
     check(lib().uw_moe_layer(gw, gd, uw_, ud, dw, dd, experts, F, H, X.data_ptr(), ldx, tokens, logits.data_ptr(), kind,
                              ldl, top_k, 1 if renormalize else 0, res, res_type, ldr, out.data_ptr(), out_type, ldo,

@@ -482,6 +482,38 @@ def test_grouped_scratch(torch_cuda):
                 check(torch, uw.gemm_grouped(W, X, off, order, 2, scratch=t)[at.cuda()], v, err, what)
 
 
+def test_no_room_for_scratch(torch_cuda, monkeypatch):
+    """Where memory has no room for what would make a call faster, it runs with what it needs."""
+    torch = torch_cuda
+    print_case("no room for scratch")
+    E, F, H, tokens = 2, 1024, 1088, 8000
+    G, U = (make_weight(torch, i, E, F, H, True)[0] for i in range(2))
+    D, _ = make_weight(torch, 2, E, H, F, True)
+    X = rows_of(torch, 1, tokens, H)
+    logits = torch.randn(tokens, E).cuda()
+    least = uw.moe_scratch_bytes(tokens, E, 1, F, H)
+    assert uw.moe_scratch_bytes(tokens, E, 1, F, H, True) > least
+    assert uw.lib().uw_linear_scratch_bytes(1, E * F, H, tokens) > 0
+    r = uw.moe_route(logits, 1)
+    calls = (lambda: uw.moe_layer(G, U, D, X, logits, 1), lambda: uw.moe_gate_up(G, U, X, r.offsets, r.order, 1),
+             lambda: uw.linear(G, X))
+    want = [f() for f in calls]
+    empty = torch.empty
+
+    def small(*a, dtype=None, **kw):
+        if dtype == torch.uint8 and a[0] > least:
+            raise torch.cuda.OutOfMemoryError("no room")
+        return empty(*a, dtype=dtype, **kw)
+    monkeypatch.setattr(torch, "empty", small)
+    least_linear, least = least, 0
+    for f, w in zip(calls[1:], want[1:]):
+        got = f()
+        assert float((got.float() - w.float()).norm() / w.float().norm()) < 2 ** -8      # half a step of bf16 each
+    least = least_linear
+    got = calls[0]()
+    assert float((got - want[0]).norm() / want[0].norm()) < 2 ** -8
+
+
 def test_grouped_bad_offsets_stay_inside(torch_cuda):
     """Offsets out of order or out of range and indexes outside X: rows outside the output's are untouched."""
     torch = torch_cuda
