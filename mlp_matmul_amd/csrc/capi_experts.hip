@@ -181,7 +181,7 @@ LayerLayout layer_layout(bool pal, int64_t tokens, int experts, int64_t top_k, i
     l.order = take(slots * 4);
     l.place = take(slots * 4);
     l.route = take(route_scratch(tokens, experts));
-    l.h = take(slots * uint64_t(F) * 2);
+    l.h = take(slots * uint64_t(F) * 2);             // bf16: what the matrix units that multiply it take
     l.y = take(slots * uint64_t(H) * 4);
     l.total = off;
     l.expand = std::max(uwk::grouped_scratch(pal, true, experts, F, H, int64_t(slots), uw::device_cus()),

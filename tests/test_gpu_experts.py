@@ -4,7 +4,7 @@ against plain definitions in 64 bits, and of a run of them together.
 Tolerances.  Products of two bf16 numbers are exact in fp32; a sum of K of
 them in any order, each addition off by at most 2^-23 of the sum of absolute
 values S, is within (K + 8) 2^-23 S.  An activation's slope is at most 1.13;
-its own evaluation (expf, erff, tanhf and a division, a few fp32 steps each)
+its own evaluation (an exponential or erff, and a division, a few fp32 steps each)
 adds at most 2^-20 |v| + 2^-20 |act(v)|.  A residual's addition is one fp32 rounding.
 The final rounding to a type t is half a step, finfo(t).eps / 2 of the value.
 """
@@ -155,6 +155,23 @@ def test_linear_in_place_residual_and_gaps(torch_cuda):
         got = uw.linear(W, X, residual=base[:, :rows], out=base[:, :rows])
         assert got.data_ptr() == base.data_ptr()
         assert torch.equal(base[:, :rows], separate) and torch.equal(base[:, rows:], keep[:, rows:])
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_activation_extremes(torch_cuda, act):
+    """The activations from the smallest to the largest numbers, through the identity: every product but one is 0."""
+    torch = torch_cuda
+    x = torch.zeros(128, dtype=torch.bfloat16)
+    big = torch.tensor([2.0 ** e for e in (-100, -20, -3, 0, 2, 4, 5, 6, 6.5, 7, 8, 13, 40, 60, 100, 127)]).bfloat16()
+    x[:16], x[16:32] = big, -big
+    x[32:] = torch.linspace(-12, 12, 96).bfloat16()
+    W = torch.eye(128, dtype=torch.bfloat16).cuda()
+    want = activate(torch, f64(x), act)
+    for batch in (1, 3, 40, 300):
+        print_case(f"{act} extremes, batch {batch}")
+        out = uw.linear(W, x[None].repeat(batch, 1).cuda(), act=act)
+        check(torch, out, want[None].expand(batch, -1), (2.0 ** -20 * (f64(x).abs() + want.abs()))[None].expand(batch, -1),
+              "extremes")
 
 
 def test_linear_infinities(torch_cuda):
