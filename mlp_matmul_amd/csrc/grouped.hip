@@ -116,10 +116,10 @@ struct TileCost {
     int mt, nt, per_cu;
     double few, one, full, launch, around, stream, again;
 };
-constexpr TileCost kTiles[TILE_SHAPES] = {{64, 64, 2, 0.18, 0.28, 0.45, 4.8, 6.2, 4.8e6, 0.53},
-                                          {128, 64, 2, 0.31, 0.48, 0.67, 4.6, 5.5, 5.1e6, 0.43},
-                                          {256, 128, 1, 0.63, 0.88, 0.88, 4.8, 7.6, 4.9e6, 0.30},
-                                          {256, 256, 1, 1.1, 1.5, 1.5, 6.3, 6.1, 5.7e6, 1.1}};
+constexpr TileCost kTiles[TILE_SHAPES] = {{64, 64, 2, 0.18, 0.28, 0.45, 4.7, 7.2, 4.8e6, 0.53},
+                                          {128, 64, 2, 0.30, 0.48, 0.69, 4.6, 6.1, 5.0e6, 0.43},
+                                          {256, 128, 1, 0.62, 0.93, 0.93, 4.9, 7.6, 4.8e6, 0.35},
+                                          {256, 256, 1, 1.1, 1.5, 1.5, 5.8, 6.9, 5.7e6, 1.1}};
 constexpr TileCost kPalTiles[PAL_TILE_SHAPES] = {{64, 64, 3, 0.52, 0.62, 0.97, 4.6, 5.3, 3.3e6, 0.73},
                                                  {128, 64, 2, 0.71, 0.90, 1.1, 3.1, 6.8, 3.1e6, 0.64},
                                                  {128, 128, 2, 0.93, 1.1, 1.7, 6.1, 3.2, 2.9e6, 0.80}};
@@ -136,10 +136,10 @@ constexpr SkinnyCost kSkinny[2][2][3] = {      // palette, pair, rows
     {{{0.52, 2.2, 4.2, 2.1, 5.3e6, 0.14}, {0.66, 1.2, 3.8, 2.9, 3.9e6, 0.62}, {0.59, 1.0, 3.2, 3.4, 2.4e6, 0.30}},
      {{0.37, 1.7, 3.2, 5.2, 3.8e6, 0.20}, {0.52, 1.2, 4.6, 4.1, 3.1e6, 0.34}, {0.29, 1.5, 7.4, 3.9, 3.0e6, 0.32}}}};
 // The tiled matmul of gemm_lds.hip into scratch: a step by its tiles' rows.
-constexpr double kSums[3] = {0.64, 1.0, 1.8}, kSumsLaunch = 6.9, kSumsAround = 2.3, kSumsStream = 5.5e6;
+constexpr double kSums[3] = {0.64, 1.1, 1.9}, kSumsLaunch = 6.4, kSumsAround = 2.9, kSumsStream = 5.5e6;
 // What expanding one matrix or a pair adds, and the bytes a us; the launch that
 // adds slices, and the bytes a us of writing and reading them.
-constexpr double kExpandLaunch[2] = {4.6, 6.9}, kExpandStream = 6.4e6, kAddLaunch = 3.1, kSliceStream = 5e6;
+constexpr double kExpandLaunch[2] = {4.6, 6.3}, kExpandStream = 6.4e6, kAddLaunch = 3.1, kSliceStream = 7e6;
 
 struct Choice {
     enum Kernel { SKINNY, TILE, PAL_TILE, SUMS, EXPAND } kernel;
