@@ -228,7 +228,7 @@ Choice choose(const Problem& p, uint64_t scratch_bytes) {
 
 // bf16 tiles of one matrix.  A few rows behind the last whole tile go to the
 // skinny kernel where they would start another round of tiles (2049 rows of
-// 4096 x 4096: 61 + 9 us against 95).
+// 4096 x 4096: 69 + 8 us against 95).
 hipError_t linear_tiles(const GroupArgs& a, const Choice& c, void* sums, hipStream_t s) {
     const int64_t tail = a.n % 128;                      // 128 and 256 both divide what is left
     if (tail && tail <= 32 && a.n > 256) {
