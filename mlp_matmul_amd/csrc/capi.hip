@@ -59,6 +59,7 @@ using uw::check_dmat;
 using uw::device_cus;
 using uw::hip_fail;
 using uw::pack_palette;
+using uw::vexp_of;
 
 int check_decoder_inputs(const uw_dmat* d, const char* who, bool need_sm) {
     int rc = check_dmat(d, who);
@@ -83,7 +84,7 @@ uwk::DecodeArgs decode_args(const uw_dmat* d, void* out) {
     a.glen = d->glen;
     a.tile_off = d->tile_off;
     a.tile_vbase = d->tile_vbase;
-    a.vexp = d->vexp;
+    a.vexp = vexp_of(d);
     a.bitmap = d->bitmap;
     a.dlut = d->dlut;
     a.mlut = d->mlut;
@@ -208,7 +209,7 @@ uwk::MatArgs compressed_args(const uw_dmat* d, const void* w, const uint16_t* X,
     uwk::MatArgs a{};
     a.w = w;
     a.sm = d->sm;
-    a.vexp = d->vexp;
+    a.vexp = vexp_of(d);
     a.bitmap = d->bitmap;
     a.tile_vbase = d->tile_vbase;
     a.X = X;

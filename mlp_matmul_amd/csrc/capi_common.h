@@ -30,6 +30,10 @@ inline void pack_palette(const uint8_t pal[16], uint32_t out[4]) {
 // Shape and size checks of a descriptor (defined with the matmul entry points).
 int check_dmat(const uw_dmat* d, const char* who);
 
+// The raw exponents, NULL without verbatim groups: the section is empty then,
+// and kernels whose lanes load from its start take another address for NULL.
+inline const uint8_t* vexp_of(const uw_dmat* d) { return d->verbatim_groups ? d->vexp : nullptr; }
+
 // Compute units of the current device (256 if it cannot be queried).
 int device_cus();
 

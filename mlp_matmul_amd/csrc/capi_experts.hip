@@ -68,7 +68,7 @@ int take_weight(const uint16_t* w, const uw_dmat* d, int64_t experts, int64_t ro
         return bad(who, "misaligned section of the compressed matrix");
     out->w = d->nib;
     out->sm = d->sm;
-    out->vexp = d->vexp ? d->vexp : d->sm;     // never read as exponents without verbatim groups
+    out->vexp = uw::vexp_of(d) ? d->vexp : d->sm;   // never read as exponents without verbatim groups
     out->bitmap = d->bitmap;
     out->tile_vbase = d->tile_vbase;
     uw::pack_palette(d->palette, out->pal);
