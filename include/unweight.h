@@ -411,8 +411,9 @@ int uw_mlp_layer(const uw_dmat* gate, const uw_dmat* up, const uw_dmat* down, in
  * the X of a matmul); sums are fp32 and rounded once, to the output's type.
  * Outputs may have any row stride of at least their width; elements between
  * the rows are left as they were.  UW_EINVAL: a shape, stride, type, NULL or
- * misaligned pointer (16 bytes), a scratch too small, an output that overlaps
- * an input it must not; UW_EUNSUPPORTED: 2^31 weights or more in a matrix.
+ * misaligned pointer (16 bytes), a scratch that is too small or overlaps what the
+ * call reads (weights and their sections, offsets and order among it) or writes,
+ * an output that overlaps an input it must not; UW_EUNSUPPORTED: 2^31 weights or more in a matrix.
  * Nothing is allocated, no call waits for the device, and every call may be
  * captured into a graph. */
 enum { UW_F32 = 0, UW_BF16 = 1 };                  /* value types */

@@ -41,10 +41,28 @@ bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
     return na && nb && x < y + nb && y < x + na;
 }
 
+// The memory that a call reads.
+struct Inputs {
+    struct {
+        const void* p;
+        uint64_t bytes;
+    } span[24];
+    int count = 0;
+
+    void add(const void* p, uint64_t bytes) {
+        if (p && bytes) span[count++] = {p, bytes};
+    }
+    bool meet(const void* p, uint64_t bytes) const {
+        for (int i = 0; i < count; ++i)
+            if (overlap(p, bytes, span[i].p, span[i].bytes)) return true;
+        return false;
+    }
+};
+
 // The weight of an operator: exactly one of w (bf16) and d (compressed, with
 // its NIB section), [experts*rows, cols].
 int take_weight(const uint16_t* w, const uw_dmat* d, int64_t experts, int64_t rows, int64_t cols, uwk::Weight* out,
-                const char* who) {
+                Inputs* in, const char* who) {
     *out = uwk::Weight{};
     if (rows < 0 || cols < uw::kGroup || cols % uw::kGroup)
         return bad(who, "bad shape (cols must be a positive multiple of 64)");
@@ -54,6 +72,7 @@ int take_weight(const uint16_t* w, const uw_dmat* d, int64_t experts, int64_t ro
     if ((w != nullptr) == (d != nullptr)) return bad(who, "give a bf16 weight or a compressed one, and not both");
     if (w) {
         if (!aligned16(w)) return bad(who, "misaligned weight");
+        in->add(w, uint64_t(experts * rows * cols) * 2);
         out->w = w;
         return UW_OK;
     }
@@ -66,6 +85,11 @@ int take_weight(const uint16_t* w, const uw_dmat* d, int64_t experts, int64_t ro
     if (!aligned16(d->nib) || !aligned16(d->sm) || !aligned16(d->vexp) || !aligned16(d->bitmap) ||
         !aligned16(d->tile_vbase))
         return bad(who, "misaligned section of the compressed matrix");
+    in->add(d->nib, uint64_t(d->groups) * 32);
+    in->add(d->sm, uint64_t(d->groups) * 64);
+    in->add(d->vexp, uint64_t(d->verbatim_groups) * 64);
+    in->add(d->bitmap, uint64_t(d->tiles) * 8);
+    in->add(d->tile_vbase, uint64_t(d->tiles + 1) * 4);
     out->w = d->nib;
     out->sm = d->sm;
     out->vexp = uw::vexp_of(d) ? d->vexp : d->sm;   // never read as exponents without verbatim groups
@@ -102,15 +126,13 @@ int check_epilogue(const uwk::Epilogue& e, int64_t n, int64_t rows, const void* 
     return UW_OK;
 }
 
-// Optional scratch, which nothing else may lie in.
-int check_scratch(const void* scratch, uint64_t* bytes, const uwk::Epilogue& e, int64_t n, int64_t rows, const void* X,
-                  uint64_t x_bytes, const char* who) {
+// Optional scratch, which no input, residual or output may lie in.
+int check_scratch(const void* scratch, uint64_t* bytes, const uwk::Epilogue& e, int64_t n, int64_t rows,
+                  const Inputs& in, const char* who) {
     if (!aligned16(scratch)) return bad(who, "misaligned scratch");
     if (!scratch) *bytes = 0;
-    if (overlap(e.out, span(n, rows, e.ldo, value_bytes(e.out_type)), scratch, *bytes) ||
-        overlap(X, x_bytes, scratch, *bytes) ||
-        (e.residual && overlap(e.residual, span(n, rows, e.ldr, value_bytes(e.residual_type)), scratch, *bytes)) ||
-        (e.bias && overlap(e.bias, uint64_t(rows) * value_bytes(e.bias_type), scratch, *bytes)))
+    if (overlap(e.out, span(n, rows, e.ldo, value_bytes(e.out_type)), scratch, *bytes) || in.meet(scratch, *bytes) ||
+        (e.residual && overlap(e.residual, span(n, rows, e.ldr, value_bytes(e.residual_type)), scratch, *bytes)))
         return bad(who, "the scratch overlaps an input or out");
     return UW_OK;
 }
@@ -125,6 +147,13 @@ int check_groups(int experts, int64_t n, const int32_t* offsets, const int32_t* 
     if (!offsets || !aligned16(offsets) || !aligned16(order)) return bad(who, "NULL or misaligned offsets or order");
     if (order ? x_rows == 0 : x_rows < n) return bad(who, "X has too few rows");
     return UW_OK;
+}
+
+// What a grouped call reads beside its weights.
+void add_rows(Inputs* in, const uwk::GroupArgs& a) {
+    in->add(a.X, span(a.x_rows, a.C, a.ldx, 2));
+    in->add(a.offsets, uint64_t(a.E + 1) * 4);
+    in->add(a.order, uint64_t(a.n) * 4);
 }
 
 uwk::GroupArgs group_args(const uint16_t* X, int64_t x_rows, int64_t ldx, const int32_t* offsets, const int32_t* order,
@@ -213,14 +242,17 @@ int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols, c
     return guarded([&]() -> int {
         const char* who = "uw_linear";
         uwk::GroupArgs a = group_args(X, batch, ldx, nullptr, nullptr, 1, batch, 1, rows, cols);
-        int rc = take_weight(w, d, 1, rows, cols, &a.w[0], who);
+        Inputs in;
+        int rc = take_weight(w, d, 1, rows, cols, &a.w[0], &in, who);
         if (rc) return rc;
         if (batch < 0 || batch >= (int64_t(1) << 31)) return bad(who, "bad batch");
         if (rows == 0 || batch == 0) return UW_OK;
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {bias, residual, out, ldr, ldo, bias_type, residual_type, out_type, act};
         if ((rc = check_epilogue(a.ep, batch, rows, X, span(batch, cols, ldx, 2), who))) return rc;
-        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, batch, rows, X, span(batch, cols, ldx, 2), who))) return rc;
+        in.add(X, span(batch, cols, ldx, 2));
+        if (bias) in.add(bias, uint64_t(rows) * value_bytes(bias_type));
+        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, batch, rows, in, who))) return rc;
         const hipError_t e = uwk::launch_linear(d != nullptr, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
@@ -286,12 +318,14 @@ int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t ro
         int rc = check_groups(experts, n, offsets, order, top_k, x_rows, who);
         if (rc) return rc;
         uwk::GroupArgs a = group_args(X, x_rows, ldx, offsets, order, top_k, n, experts, rows, cols);
-        if ((rc = take_weight(w, d, experts, rows, cols, &a.w[0], who))) return rc;
+        Inputs in;
+        if ((rc = take_weight(w, d, experts, rows, cols, &a.w[0], &in, who))) return rc;
         if (rows == 0 || n == 0) return UW_OK;
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {nullptr, nullptr, out, 0, ldo, UW_F32, UW_F32, out_type, UW_ACT_NONE};
         if ((rc = check_epilogue(a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
-        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
+        add_rows(&in, a);
+        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, in, who))) return rc;
         const hipError_t e = uwk::launch_grouped(d != nullptr, false, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
@@ -306,14 +340,16 @@ int uw_moe_gate_up(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t
         int rc = check_groups(experts, n, offsets, order, top_k, x_rows, who);
         if (rc) return rc;
         uwk::GroupArgs a = group_args(X, x_rows, ldx, offsets, order, top_k, n, experts, rows, cols);
-        if ((rc = take_weight(gate_w, gate_d, experts, rows, cols, &a.w[0], who))) return rc;
-        if ((rc = take_weight(up_w, up_d, experts, rows, cols, &a.w[1], who))) return rc;
+        Inputs in;
+        if ((rc = take_weight(gate_w, gate_d, experts, rows, cols, &a.w[0], &in, who))) return rc;
+        if ((rc = take_weight(up_w, up_d, experts, rows, cols, &a.w[1], &in, who))) return rc;
         if ((gate_d != nullptr) != (up_d != nullptr)) return bad(who, "gate and up must both be bf16 or both compressed");
         if (rows == 0 || n == 0) return UW_OK;
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {nullptr, nullptr, h, 0, ldh, UW_F32, UW_F32, UW_BF16, UW_ACT_NONE};
         if ((rc = check_epilogue(a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
-        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
+        add_rows(&in, a);
+        if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, in, who))) return rc;
         const hipError_t e = uwk::launch_grouped(gate_d != nullptr, true, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
     });
@@ -369,9 +405,10 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         if (rows < uw::kGroup || cols < uw::kGroup || rows % uw::kGroup || cols % uw::kGroup)
             return bad(who, "gate and up are [rows, cols], down [cols, rows], rows and cols positive multiples of 64");
         uwk::Weight probe, down;
-        if ((rc = take_weight(gate_w, gate_d, experts, rows, cols, &probe, who)) ||
-            (rc = take_weight(up_w, up_d, experts, rows, cols, &probe, who)) ||
-            (rc = take_weight(down_w, down_d, experts, cols, rows, &down, who)))
+        Inputs in;
+        if ((rc = take_weight(gate_w, gate_d, experts, rows, cols, &probe, &in, who)) ||
+            (rc = take_weight(up_w, up_d, experts, rows, cols, &probe, &in, who)) ||
+            (rc = take_weight(down_w, down_d, experts, cols, rows, &down, &in, who)))
             return rc;
         if ((gate_d != nullptr) != (up_d != nullptr)) return bad(who, "gate and up must both be bf16 or both compressed");
         if (tokens == 0) return UW_OK;
@@ -384,7 +421,9 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         const LayerLayout l = layer_layout(gate_d || down_d, tokens, experts, top_k, rows, cols);
         if (!scratch || !aligned16(scratch) || scratch_bytes < l.total)
             return bad(who, "scratch smaller than uw_moe_scratch_bytes()");
-        if ((rc = check_scratch(scratch, &scratch_bytes, ep, tokens, cols, X, span(tokens, cols, ldx, 2), who))) return rc;
+        in.add(X, span(tokens, cols, ldx, 2));
+        in.add(logits, span(tokens, experts, ldl, value_bytes(logits_type)));
+        if ((rc = check_scratch(scratch, &scratch_bytes, ep, tokens, cols, in, who))) return rc;
         uint8_t* const base = static_cast<uint8_t*>(scratch);
         int32_t* const ids = reinterpret_cast<int32_t*>(base + l.ids);
         float* const weights = reinterpret_cast<float*>(base + l.weights);

@@ -1,0 +1,57 @@
+"""Scratch and outputs that lie in what a call reads are refused before any
+launch: placeholder device pointers, no GPU."""
+import ctypes as ct
+
+import mlp_matmul_amd as uw
+from mlp_matmul_amd import _capi
+from tests.test_experts_launches import dmat, info_of
+from tests.test_experts_refusals import at, gate_up, grouped, layer, linear
+
+
+class _Library:
+    lib = uw.lib()
+
+
+def planes(rows, cols, verbatim=40):
+    """A descriptor of placeholder sections, and {section: (address, bytes)}."""
+    d = dmat(_Library, info_of(rows, cols, verbatim))
+    n = rows * cols
+    sizes = {"sm": n, "nib": n // 2, "vexp": 64 * verbatim, "bitmap": 8 * d.tiles, "tile_vbase": 4 * (d.tiles + 1)}
+    return d, {k: (at(20 + _capi.SECTION_NAMES.index(k)), v) for k, v in sizes.items()}
+
+
+def inside(address, size):
+    """Its first 16 bytes and those that hold its last byte."""
+    return address, address + (size - 1) // 16 * 16
+
+
+def test_scratch_in_an_input():
+    def refused(f, address, size, **kw):
+        for p in inside(address, size):
+            assert f(**{"scratch": p, "sb": 16, **kw}) == _capi.UW_EINVAL, (f.__name__, hex(address), size)
+            assert b"scratch overlaps" in uw.lib().uw_last_error()
+
+    # weights [128, 256] and experts' [4, 64, 128] (down [4, 128, 64]) in bf16
+    refused(linear, at(1), 128 * 256 * 2)
+    refused(grouped, at(1), 4 * 64 * 128 * 2)
+    for i in (1, 2):
+        refused(gate_up, at(i), 4 * 64 * 128 * 2)
+    # the groups: offsets of 4 experts, an order of 40 rows
+    refused(grouped, at(3), 5 * 4)
+    refused(grouped, at(4), 40 * 4)
+    refused(gate_up, at(4), 5 * 4)
+    refused(gate_up, at(5), 40 * 4)
+    # a layer's needs its scratch whole: it ends behind the input's first bytes, or starts in its last ones
+    need = uw.lib().uw_moe_scratch_bytes(0, 20, 4, 2, 64, 128)
+    for i, size in ((1, 4 * 64 * 128 * 2), (2, 4 * 64 * 128 * 2), (3, 4 * 64 * 128 * 2), (4, 20 * 128 * 2), (5, 20 * 4 * 4)):
+        for p in (at(i) + 16 - need, inside(at(i), size)[1]):
+            assert layer(scratch=p, sb=need) == _capi.UW_EINVAL, i
+            assert b"scratch overlaps" in uw.lib().uw_last_error()
+    # compressed weights: every section
+    d, sections = planes(256, 128)
+    for address, size in sections.values():
+        refused(grouped, address, size, w=None, d=ct.byref(d))
+        refused(gate_up, address, size, gw=None, gd=ct.byref(d), uw_=None, ud=ct.byref(d))
+    d, sections = planes(128, 256)
+    for address, size in sections.values():
+        refused(linear, address, size, w=None, d=ct.byref(d))
