@@ -107,8 +107,8 @@ int check_rows(const void* p, int64_t ld, int64_t cols, int64_t multiple, const 
     return UW_OK;
 }
 
-// out (and the residual it may replace) against what the call reads.
-int check_epilogue(const uwk::Epilogue& e, int64_t n, int64_t rows, const void* X, uint64_t x_bytes, const char* who) {
+// out (and the residual it may replace) against what the call reads while out is written.
+int check_epilogue(const uwk::Epilogue& e, int64_t n, int64_t rows, const Inputs& in, const char* who) {
     if (!value_type(e.out_type) || (e.bias && !value_type(e.bias_type)) || (e.residual && !value_type(e.residual_type)))
         return bad(who, "a value type is neither UW_F32 nor UW_BF16");
     if (e.act < 0 || e.act >= uwk::ACT_COUNT) return bad(who, "unknown activation");
@@ -117,9 +117,7 @@ int check_epilogue(const uwk::Epilogue& e, int64_t n, int64_t rows, const void* 
     if (e.residual && (rc = check_rows(e.residual, e.ldr, rows, 1, who, "residual"))) return rc;
     if (e.bias && !aligned16(e.bias)) return bad(who, "misaligned bias");
     const uint64_t ob = span(n, rows, e.ldo, value_bytes(e.out_type));
-    if (overlap(e.out, ob, X, x_bytes)) return bad(who, "out overlaps the input");
-    if (e.bias && overlap(e.out, ob, e.bias, uint64_t(rows) * value_bytes(e.bias_type)))
-        return bad(who, "out overlaps the bias");
+    if (in.meet(e.out, ob)) return bad(who, "out overlaps an input");
     if (e.residual && overlap(e.out, ob, e.residual, span(n, rows, e.ldr, value_bytes(e.residual_type))) &&
         (e.out != e.residual || e.ldo != e.ldr || e.out_type != e.residual_type))
         return bad(who, "out overlaps the residual without being it");
@@ -249,9 +247,9 @@ int uw_linear(const uint16_t* w, const uw_dmat* d, int64_t rows, int64_t cols, c
         if (rows == 0 || batch == 0) return UW_OK;
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {bias, residual, out, ldr, ldo, bias_type, residual_type, out_type, act};
-        if ((rc = check_epilogue(a.ep, batch, rows, X, span(batch, cols, ldx, 2), who))) return rc;
         in.add(X, span(batch, cols, ldx, 2));
-        if (bias) in.add(bias, uint64_t(rows) * value_bytes(bias_type));
+        in.add(bias, uint64_t(rows) * value_bytes(bias_type));
+        if ((rc = check_epilogue(a.ep, batch, rows, in, who))) return rc;
         if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, batch, rows, in, who))) return rc;
         const hipError_t e = uwk::launch_linear(d != nullptr, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
@@ -323,8 +321,8 @@ int uw_gemm_grouped(const uint16_t* w, const uw_dmat* d, int experts, int64_t ro
         if (rows == 0 || n == 0) return UW_OK;
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {nullptr, nullptr, out, 0, ldo, UW_F32, UW_F32, out_type, UW_ACT_NONE};
-        if ((rc = check_epilogue(a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
         add_rows(&in, a);
+        if ((rc = check_epilogue(a.ep, n, rows, in, who))) return rc;
         if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, in, who))) return rc;
         const hipError_t e = uwk::launch_grouped(d != nullptr, false, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
@@ -347,8 +345,8 @@ int uw_moe_gate_up(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t
         if (rows == 0 || n == 0) return UW_OK;
         if ((rc = check_rows(X, ldx, cols, 8, who, "X"))) return rc;
         a.ep = {nullptr, nullptr, h, 0, ldh, UW_F32, UW_F32, UW_BF16, UW_ACT_NONE};
-        if ((rc = check_epilogue(a.ep, n, rows, X, span(x_rows, cols, ldx, 2), who))) return rc;
         add_rows(&in, a);
+        if ((rc = check_epilogue(a.ep, n, rows, in, who))) return rc;
         if ((rc = check_scratch(scratch, &scratch_bytes, a.ep, n, rows, in, who))) return rc;
         const hipError_t e = uwk::launch_grouped(gate_d != nullptr, true, a, scratch, scratch_bytes, as_stream(stream));
         return e == hipSuccess ? UW_OK : hip_fail(e, who);
@@ -368,7 +366,11 @@ int uw_moe_combine(const float* Y, int64_t n, int64_t cols, const int32_t* place
         if ((n && (!Y || !aligned16(Y))) || !place || !weights || !aligned16(place) || !aligned16(weights))
             return bad(who, "NULL or misaligned Y, place or weights");
         const uwk::Epilogue ep{nullptr, residual, out, ldr, ldo, UW_F32, residual_type, out_type, UW_ACT_NONE};
-        int rc = check_epilogue(ep, tokens, cols, Y, span(n, cols, cols, 4), who);
+        Inputs in;
+        in.add(Y, span(n, cols, cols, 4));
+        in.add(place, uint64_t(tokens) * top_k * 4);
+        in.add(weights, uint64_t(tokens) * top_k * 4);
+        int rc = check_epilogue(ep, tokens, cols, in, who);
         if (rc) return rc;
         const uwk::CombineArgs a{Y, place, nullptr, weights, n, cols, tokens, top_k, residual, out, ldr, ldo,
                                  residual_type, out_type};
@@ -415,9 +417,9 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
         if ((rc = check_rows(X, ldx, cols, 8, who, "X")) || (rc = check_rows(logits, ldl, experts, 1, who, "logits")))
             return rc;
         if (!value_type(logits_type)) return bad(who, "logits are UW_F32 or UW_BF16");
-        // out is written by the last step alone: it may be X or the residual
+        // out is written by the last step alone, which reads down: it may be X or the residual
         const uwk::Epilogue ep{nullptr, residual, out, ldr, ldo, UW_F32, residual_type, out_type, UW_ACT_NONE};
-        if ((rc = check_epilogue(ep, tokens, cols, nullptr, 0, who))) return rc;
+        if ((rc = check_epilogue(ep, tokens, cols, in, who))) return rc;
         const LayerLayout l = layer_layout(gate_d || down_d, tokens, experts, top_k, rows, cols);
         if (!scratch || !aligned16(scratch) || scratch_bytes < l.total)
             return bad(who, "scratch smaller than uw_moe_scratch_bytes()");

@@ -5,7 +5,7 @@ import ctypes as ct
 import mlp_matmul_amd as uw
 from mlp_matmul_amd import _capi
 from tests.test_experts_launches import dmat, info_of
-from tests.test_experts_refusals import at, gate_up, grouped, layer, linear
+from tests.test_experts_refusals import at, combine, gate_up, grouped, layer, linear
 
 
 class _Library:
@@ -55,3 +55,29 @@ def test_scratch_in_an_input():
     d, sections = planes(128, 256)
     for address, size in sections.values():
         refused(linear, address, size, w=None, d=ct.byref(d))
+
+
+def test_out_in_an_input():
+    def refused(f, address, size, out="out", **kw):
+        for p in inside(address, size):
+            assert f(**{out: p, **kw}) == _capi.UW_EINVAL, (f.__name__, hex(address), size)
+            assert b"out overlaps" in uw.lib().uw_last_error()
+
+    refused(linear, at(1), 128 * 256 * 2)
+    refused(linear, at(2), 4 * 256 * 2)
+    refused(linear, at(3), 128 * 4)
+    refused(grouped, at(1), 4 * 64 * 128 * 2)
+    refused(grouped, at(2), 20 * 128 * 2)
+    refused(grouped, at(3), 5 * 4)
+    refused(grouped, at(4), 40 * 4)
+    for i, size in ((1, 4 * 64 * 128 * 2), (2, 4 * 64 * 128 * 2), (3, 20 * 128 * 2), (4, 5 * 4), (5, 40 * 4)):
+        refused(gate_up, at(i), size, "h")
+    refused(combine, at(1), 40 * 64 * 4)
+    refused(combine, at(2), 20 * 2 * 4)
+    refused(combine, at(3), 20 * 2 * 4)
+    for i in (1, 2, 3):
+        refused(layer, at(i), 4 * 64 * 128 * 2)
+    d, sections = planes(256, 128)
+    for address, size in sections.values():
+        refused(grouped, address, size, w=None, d=ct.byref(d))
+        refused(gate_up, address, size, "h", gw=None, gd=ct.byref(d), uw_=None, ud=ct.byref(d))
