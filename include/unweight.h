@@ -458,6 +458,7 @@ int64_t uw_linear_scratch_bytes(int compressed, int64_t rows, int64_t cols, int6
  * largest finite number.  A token with fewer than top_k others (a padded one
  * has none) gets id -1, weight 0 and place -1 in its last slots; order is -1
  * behind the last row.  experts <= 512, top_k <= 16, tokens * top_k < 2^31.
+ * Logits, outputs and scratch overlap nowhere.
  * scratch: uw_moe_route_scratch_bytes() bytes (0 through 64 tokens); calls that
  * share it must be ordered. */
 int uw_moe_route(const void* logits, int logits_type, int64_t ld, int64_t tokens, int experts,

@@ -3,6 +3,7 @@
 // for the contract.
 #include <algorithm>
 #include <exception>
+#include <utility>
 
 #include "capi_common.h"
 #include "experts.h"
@@ -41,7 +42,7 @@ bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
     return na && nb && x < y + nb && y < x + na;
 }
 
-// The memory that a call reads.
+// Memory that a call reads (or writes).
 struct Inputs {
     struct {
         const void* p;
@@ -285,6 +286,16 @@ int uw_moe_route(const void* logits, int logits_type, int64_t ld, int64_t tokens
         const uint64_t need = route_scratch(tokens, experts);
         if (need && (!scratch || !aligned16(scratch) || scratch_bytes < need))
             return bad(who, "scratch smaller than uw_moe_route_scratch_bytes()");
+        // every block reads its logits while others write: nothing shares memory
+        const uint64_t slots = uint64_t(tokens) * uint64_t(top_k) * 4;
+        const std::pair<const void*, uint64_t> writes[] = {{ids, slots},   {weights, slots}, {offsets, uint64_t(experts + 1) * 4},
+                                                           {order, slots}, {place, slots},   {scratch, need}};
+        Inputs others;
+        others.add(logits, span(tokens, experts, ld, value_bytes(logits_type)));
+        for (const auto& w : writes) {
+            if (others.meet(w.first, w.second)) return bad(who, "an output or the scratch overlaps another or the logits");
+            others.add(w.first, w.second);
+        }
         uwk::RouteArgs a{logits, ld,  tokens,  logits_type, experts, top_k, renormalize != 0, ids, weights,
                          offsets, order, place, static_cast<uint16_t*>(scratch), 0, 0};
         uwk::route_blocks(tokens, &a.blocks, &a.per_block);

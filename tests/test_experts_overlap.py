@@ -5,7 +5,7 @@ import ctypes as ct
 import mlp_matmul_amd as uw
 from mlp_matmul_amd import _capi
 from tests.test_experts_launches import dmat, info_of
-from tests.test_experts_refusals import at, combine, gate_up, grouped, layer, linear
+from tests.test_experts_refusals import at, combine, gate_up, grouped, layer, linear, route
 
 
 class _Library:
@@ -81,3 +81,17 @@ def test_out_in_an_input():
     for address, size in sections.values():
         refused(grouped, address, size, w=None, d=ct.byref(d))
         refused(gate_up, address, size, "h", gw=None, gd=ct.byref(d), uw_=None, ud=ct.byref(d))
+
+
+def test_routing_outputs_share_nothing():
+    slots, offsets = 100 * 2 * 4, 9 * 4
+    need = uw.lib().uw_moe_route_scratch_bytes(100, 8, 2)
+    spans = {"ids": (at(2), slots), "weights": (at(3), slots), "off": (at(4), offsets), "order": (at(5), slots),
+             "place": (at(6), slots), "scratch": (at(7), need)}
+    for name, (_, size) in spans.items():
+        for other, (address, length) in {**spans, "logits": (at(1), 100 * 8 * 4)}.items():
+            if other != name:
+                # over its last bytes, and ending in its first ones
+                for p in (inside(address, length)[1], address + 16 - -(-size // 16) * 16):
+                    assert route(**{name: p}) == _capi.UW_EINVAL, (name, other)
+                    assert b"overlaps" in uw.lib().uw_last_error()
