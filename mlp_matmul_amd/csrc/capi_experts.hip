@@ -396,9 +396,10 @@ int64_t uw_moe_scratch_bytes(int compressed, int64_t tokens, int experts, int to
         const char* who = "uw_moe_scratch_bytes";
         int r = check_routing(tokens, experts, top_k, who);
         if (r) return r;
-        if (rows < uw::kGroup || cols < uw::kGroup || rows % uw::kGroup || cols % uw::kGroup ||
-            rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31))
+        if (rows < uw::kGroup || cols < uw::kGroup || rows % uw::kGroup || cols % uw::kGroup)
             return bad(who, "rows and cols must be positive multiples of 64");
+        if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows * cols >= (int64_t(1) << 31))
+            return fail(UW_EUNSUPPORTED, std::string(who) + ": a matrix of 2^31 weights or more");
         const LayerLayout l = layer_layout(compressed != 0, tokens, experts, top_k, rows, cols);
         out = int64_t(l.total + l.expand);
         return UW_OK;

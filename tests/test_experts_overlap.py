@@ -95,3 +95,11 @@ def test_routing_outputs_share_nothing():
                 for p in (inside(address, length)[1], address + 16 - -(-size // 16) * 16):
                     assert route(**{name: p}) == _capi.UW_EINVAL, (name, other)
                     assert b"overlaps" in uw.lib().uw_last_error()
+
+
+def test_layer_scratch_of_matrices_that_no_call_takes():
+    """2^31 weights or more in a matrix: an error code, as the layer itself gives, and no wrapped size."""
+    for rows, cols in ((1 << 16, 1 << 15), (64, (1 << 31) - 64), ((1 << 31) - 64, (1 << 31) - 64)):
+        for tokens in (1, (1 << 31) - 1):
+            assert uw.lib().uw_moe_scratch_bytes(0, tokens, 8, 1, rows, cols) == _capi.UW_EUNSUPPORTED, (rows, cols)
+    assert uw.lib().uw_moe_scratch_bytes(0, (1 << 31) - 1, 8, 1, 64, (1 << 25) - 64) > 1 << 57
