@@ -128,6 +128,8 @@ class DeviceMatrix:
     """A compressed matrix with the chosen sections copied to device memory
     (torch uint8 buffers, 16-byte padded) and its uw_dmat descriptor."""
 
+    requires_grad = False              # as a tensor's
+
     def __init__(self, blob: Blob, sections, device="cuda"):
         torch = _torch()
         self.info = blob.info()
@@ -350,7 +352,9 @@ def silu_mul_bf16(g, u, h=None, stream=None):
 # A weight is a contiguous bf16 tensor or a DeviceMatrix with the sections of
 # the direct-palette form.  Tensors of a call are on one device, which need
 # not be the current one; the call runs on that device's current stream, or on
-# `stream` (a raw handle), where its outputs are allocated too.
+# `stream` (a raw handle), where its outputs are allocated too.  There is no
+# backward pass: tensors that require a gradient are refused outside
+# torch.no_grad().
 class Routing(NamedTuple):
     """What moe_route returns: the experts and weights of every token, and its
     slots grouped by expert (uw_moe_route)."""
@@ -408,13 +412,20 @@ def _weight_arg(W, experts, name="W"):
 
 
 def _one_device(first, *others):
-    """The device all of them are on (None entries are left out)."""
+    """The device all of them are on (None entries are left out).  None of them
+    may ask for a gradient: there is no backward pass."""
     dev = first.device
     if dev.type != "cuda":
         raise ValueError("the tensors must be on a GPU")
+    grad = first.requires_grad
     for t in others:
-        if t is not None and t.device != dev:
+        if t is None:
+            continue
+        if t.device != dev:
             raise ValueError(f"tensors on {dev} and {t.device}: a call takes one device")
+        grad = grad or t.requires_grad
+    if grad and _torch().is_grad_enabled():
+        raise ValueError("a tensor requires a gradient and there is no backward pass: call under torch.no_grad()")
     return dev
 
 
