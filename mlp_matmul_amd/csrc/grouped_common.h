@@ -117,8 +117,12 @@ __device__ __forceinline__ const uint16_t* group_x_row(const GroupArgs& a, int64
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
 // x / (1 + exp(-x)) from the hardware's base-2 exponential and reciprocal, each
-// within one unit in the last place: a rounding of -x log2(e) is worth |x| 2^-24
-// of exp(-x), which counts where exp(-x) is not small against 1 and |x| is.
+// within one unit in the last place.  The rounding of -x log2(e), and of log2(e),
+// moves the exponent by 1.225 |x| 2^-24: no more than x off by 1.225 half steps
+// would, which the fp32 sum that x is already is off by.  So the result, to (1.225 |x| +
+// 6) 2^-24 of itself, is SiLU of a neighbour of x; an exponential without that error would
+// take twice the instructions.  From x = -87.3 down exp(-x) passes 2^126 and the
+// result may be 0 (its size is below 2^-119).
 __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
 }
@@ -127,8 +131,10 @@ __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case ACT_RELU: return v < 0.f ? 0.f : v;           // NaN stays
         case ACT_SILU: return silu(v);
+        // (1 + erf cancels where v is below -2: within 3 min(|v|, 6) 2^-24)
         case ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-        // 1 + tanh(u) = 2 / (1 + exp(-2u))
+        // 1 + tanh(u) = 2 / (1 + exp(-2u)), without the cancellation that tanh near
+        // -1 has: within (8 |2u| + 6) 2^-24 of the result
         case ACT_GELU_TANH:
             return v * __builtin_amdgcn_rcpf(
                 1.0f + __builtin_amdgcn_exp2f(-2.0f * 1.4426950408889634f * 0.79788456080286536f * fmaf(0.044715f * v * v, v, v)));
