@@ -500,7 +500,6 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     if ctx is not None:
         with ctx:
             return linear(W, X, bias, act, residual, out, out_dtype, scratch)
-    torch = _torch()
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
     w, d, rows, cols = _weight_arg(W, None)

@@ -114,6 +114,19 @@ __device__ __forceinline__ const uint16_t* group_x_row(const GroupArgs& a, int64
     return a.X + r * a.ldx;
 }
 
+// 16 bytes a lane from memory to LDS; lane i's land at dst + 16 i.
+__device__ __forceinline__ void dma16(const void* src, void* dst) {
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// Waits until at most N vector memory operations are pending; LDS: and for every
+// LDS operation.
+template <int N, bool LDS>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (LDS ? 0 : 15 << 8));
+}
+
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
 // x / (1 + exp(-x)) from the hardware's base-2 exponential and reciprocal, each

@@ -406,12 +406,15 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_combine_kernel(GroupArgs
     }
 }
 
+// The input rows of a workgroup fit 48 KB of LDS: 24 slabs.  So do the tables of a
+// wave's tiles its 64 lanes: those of two rows in a run, or of a row of every
+// chosen expert, each with a tile that another row has a part of.
+constexpr int kStagedSlabs = 24;
+static_assert(2 * kStagedSlabs * kSlab / 4096 + 1 <= 64 && 2 * kStagedSlabs <= 64, "tiles fit the lanes");
+
 // Rows of a wave: one, or two on tall matrices (a wave's start is paid for half
-// as often; single matrices only, 65536 x 4096: 65 us against 77), as long as
-// the tables of its tiles fit its lanes.
-int rows_of_wave(const GroupArgs& a, bool pair) {
-    return !pair && a.R >= 8192 && 2 * int64_t(a.C) <= 60 * 4096 ? 2 : 1;
-}
+// as often; single matrices only, 65536 x 4096: 65 us against 77).
+int rows_of_wave(const GroupArgs& a, bool pair) { return !pair && a.R >= 8192 ? 2 : 1; }
 
 size_t staged_bytes(const GroupArgs& a, int nb) { return size_t(nb) * ((a.C + kSlab - 1) / kSlab) * kSlab * 2; }
 
@@ -432,8 +435,7 @@ hipError_t launch(const GroupArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// The input rows fit 48 KB of LDS and a wave's tiles its 64 lanes.
-bool gemv_rows_supported(const GroupArgs& a, int nb) { return staged_bytes(a, nb) <= 48 * 1024; }
+bool gemv_rows_supported(const GroupArgs& a, int nb) { return staged_bytes(a, nb) <= size_t(kStagedSlabs) * kSlab * 2; }
 
 hipError_t launch_gemv_rows(bool pal, bool pair, const GroupArgs& a, int nb, hipStream_t s) {
     if (nb == 1)
@@ -443,10 +445,7 @@ hipError_t launch_gemv_rows(bool pal, bool pair, const GroupArgs& a, int nb, hip
                : (pair ? launch<false, true, 2>(a, s) : launch<false, false, 2>(a, s));
 }
 
-// A row's tiles of every chosen expert fit the lanes, the inputs 48 KB.
-bool gemv_combine_supported(const GroupArgs& a, int top_k) {
-    return top_k * ((a.C + 4095) / 4096 + 1) <= 64 && staged_bytes(a, top_k) <= 48 * 1024;
-}
+bool gemv_combine_supported(const GroupArgs& a, int top_k) { return gemv_rows_supported(a, top_k); }
 
 hipError_t launch_gemv_combine(bool pal, const GroupArgs& a, const CombineArgs& c, hipStream_t s) {
     const dim3 grid(unsigned((a.R + kGemvWaves - 1) / kGemvWaves)), block(64 * kGemvWaves);

@@ -35,20 +35,6 @@ namespace {
 constexpr int kStepK = 128;          // columns of a step
 constexpr int kSegment = 4096;       // columns whose verbatim tables are in registers
 
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-// 16 bytes a lane from memory to LDS; lane i's land at dst + 16 i.
-__device__ __forceinline__ void dma16(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_ptr)dst, 16, 0, 0);
-}
-
-// Waits until at most N vector memory operations are pending.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
 __device__ __forceinline__ u32x4_t lds16(const uint8_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
 template <bool PAL, bool PAIR, int NRB, int XQ, int KW>
@@ -321,21 +307,21 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(GroupArgs a, uint32_t b
         issue_x(min(lo + 1u, last), 1);
         issue_v(v[1]);
         __builtin_amdgcn_sched_barrier(0);
-        wait_vm<XQ + 2 * kV>();                          // step 0 of the segment is in LDS
+        wait_vm<XQ + 2 * kV, false>();                          // step 0 of the segment is in LDS
         uint32_t s = lo;
         for (; s + D <= hi; s += D) {
 #pragma unroll
             for (int j = 0; j < D; ++j) {
-                wait_vm<kPer>();
+                wait_vm<kPer, false>();
                 compute(j, v[j], false);
                 issue(min(s + uint32_t(j + D), last), j, v[j]);
             }
         }
         if (s < hi) {
-            wait_vm<kPer>();
+            wait_vm<kPer, false>();
             compute(0, v[0], false);
         }
-        wait_vm<0>();                                    // no load lands after its slot is used again
+        wait_vm<0, false>();                                    // no load lands after its slot is used again
         lo = hi;
     }
     if (C % kStepK && wave == KW - 1) {                  // 64 columns left: the upper half multiplies zeros
@@ -347,7 +333,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(GroupArgs a, uint32_t b
             for (int r = 0; r < NRB; ++r) fl[r][0] = 0u;
         }
         issue(steps, 0, v);
-        wait_vm<0>();
+        wait_vm<0, false>();
         compute(0, v, true);
     }
 

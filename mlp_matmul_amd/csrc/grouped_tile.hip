@@ -32,19 +32,6 @@ namespace {
 
 constexpr int kStep = 64;
 
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-__device__ __forceinline__ void dma16(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_ptr)dst, 16, 0, 0);
-}
-
-// Waits until at most N loads are on their way, and for every LDS read.
-template <int N>
-__device__ __forceinline__ void wait() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
-
 template <bool PAIR, int MT, int NT, int WM, int S>
 __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t bands) {
     constexpr int WN = 2, NW = WM * WN;                  // waves across the input rows, in all
@@ -153,7 +140,7 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
         mixed();
         __builtin_amdgcn_sched_barrier(0);
         // the next step's loads and this step's fragments are here
-        wait<(S - 2) * (WD + XD)>();
+        wait_vm<(S - 2) * (WD + XD), true>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         load(s + S, i);
@@ -167,7 +154,7 @@ __global__ __launch_bounds__(128 * WM, 1) void tile_kernel(GroupArgs a, uint32_t
         load(uint32_t(i), i);
         __builtin_amdgcn_sched_barrier(0);               // in this order: the waits count them
     }
-    wait<(S - 1) * (WD + XD)>();
+    wait_vm<(S - 1) * (WD + XD), true>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read(0, 0, f0);

@@ -21,19 +21,6 @@ namespace {
 
 constexpr int kStep = 64;            // columns of a step: one group of every row
 
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-__device__ __forceinline__ void dma16(const void* src, void* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_ptr)dst, 16, 0, 0);
-}
-
-// Waits until at most N loads are on their way, and for every LDS operation.
-template <int N>
-__device__ __forceinline__ void wait() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
-
 // Exponents of the four 4-bit indices in the bytes of n by byte permutes: both
 // 8-entry halves of the palette are looked up, the index's top bit selects.
 __device__ __forceinline__ uint32_t look4(uint32_t n, const uint32_t (&pal)[4]) {
@@ -198,7 +185,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void tile_pal_kernel(GroupArgs a, 
         }
         read(i % 2, i % NS, 1, f0);
         __builtin_amdgcn_sched_barrier(0);
-        wait<kWait>();                                   // the next step's input rows have landed
+        wait_vm<kWait, true>();                                   // the next step's input rows have landed
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         load_x(s + P + 1, i % NS);
