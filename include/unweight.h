@@ -506,7 +506,9 @@ int uw_moe_combine(const float* Y, int64_t n, int64_t cols, const int32_t* place
                    void* out, int out_type, int64_t ldo, void* stream);
 
 /* A whole layer: uw_moe_route on the logits, gate/up, down on the bf16 h, and
- * the weighted sum, out[t] = sum_j w_j down_e(h_tj) + residual[t].  gate and up
+ * the weighted sum, out[t] = sum_j w_j down_e(h_tj) + residual[t].  h is rounded
+ * to bf16 whatever the number of tokens and the output's type, as in
+ * uw_mlp_layer and as the four calls in a row have it.  gate and up
  * [experts*rows, cols], down [experts*cols, rows], rows and cols multiples of
  * 64; residual may be NULL; out may be X or the residual (same stride and
  * type as the residual).  scratch: uw_moe_scratch_bytes() bytes (compressed:

@@ -494,7 +494,10 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     """uw_linear: act(X . W^T + bias) + residual in one matmul.  W [rows, cols],
     X bf16 [batch, cols] (any row stride that is a multiple of 8), bias [rows]
     and residual [batch, rows] fp32 or bf16; `out` (out_dtype, fp32 by default)
-    may be the residual itself."""
+    may be the residual itself.  `scratch` (None: allocated where it helps) is a
+    tensor of any size: for large batches of compressed weights it holds the
+    matrix as bf16 (2 bytes a weight), sums of K-slices for others; an empty one
+    saves that memory and is slower."""
     dev = _one_device(X, W, bias, residual, out, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -572,7 +575,10 @@ def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, s
     """uw_gemm_grouped: rows offsets[e] .. offsets[e+1]-1 of the result are
     X's rows (order[s] // top_k where order is given, else s) times expert e's
     matrix.  W [experts, rows, cols] or a DeviceMatrix of experts*rows rows.
-    `scratch` (None: allocated where it helps) is a tensor of any size."""
+    `scratch` (None: allocated where it helps) is a tensor of any size; for
+    compressed weights of experts with hundreds of rows it holds every expert's
+    matrix as bf16 (2 bytes a weight; the pair of moe_gate_up both matrices), an
+    empty one saves that memory and is slower."""
     dev = _one_device(X, W, offsets, order, out, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -647,7 +653,10 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     top_k experts (+ residual), the experts chosen by `logits`
     [tokens, experts].  gate, up [experts, F, H] and down [experts, H, F], or
     DeviceMatrix of experts*F and experts*H rows; `out` may be X or the
-    residual."""
+    residual.  h, between up and down, is rounded to bf16.  `scratch` (None:
+    allocated) needs moe_scratch_bytes() bytes; with compressed=True, which None
+    takes where memory has room, they hold gate and up of all experts as bf16
+    (2 bytes a weight each) for prompts."""
     dev = _one_device(X, gate, up, down, logits, residual, out, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:

@@ -209,7 +209,11 @@ LayerLayout layer_layout(bool pal, int64_t tokens, int experts, int64_t top_k, i
     l.order = take(slots * 4);
     l.place = take(slots * 4);
     l.route = take(route_scratch(tokens, experts));
-    l.h = take(slots * uint64_t(F) * 2);             // bf16: what the matrix units that multiply it take
+    // bf16, as uw_mlp_layer's: the type that the instructions that multiply it take (MFMA, and v_dot2
+    // for a single token, which a second bf16 term would double), alike for every number of tokens so
+    // that a token's result does not change with its batch.  At most half a step, 2^-8, of each h:
+    // 0.0017 of the experts' sum in the norm, what rounding the output to bf16 costs too
+    l.h = take(slots * uint64_t(F) * 2);
     l.y = take(slots * uint64_t(H) * 4);
     l.total = off;
     l.expand = std::max(uwk::grouped_scratch(pal, true, experts, F, H, int64_t(slots), uw::device_cus()),

@@ -104,7 +104,8 @@ hipError_t add_sums(const GroupArgs& a, const float* sums, int split, hipStream_
 // rows each, even and skewed), each timed on MI355X with every kernel; what the
 // estimates choose there takes 1.02 to 1.04 times the fastest kernel's time in
 // the geometric mean, by kind of product, and 1.7 times at worst.  Thresholds
-// on the rows alone took 1.05 to 1.21 times.
+// on the rows alone took 1.05 to 1.21 times.  A constant of 0 is a term that those
+// sizes did not tell from its neighbours.
 
 // Times in us: a 64-column step of a round of workgroups with one here and
 // there, with one on each compute unit, with `per_cu` on each; the launch, and

@@ -13,9 +13,9 @@
 // rows touch, one tile a lane; an item picks its 16 flags by lane reads, so
 // flags and slots cost scalar instructions, and the raw exponents come with
 // the item's other loads (lanes outside verbatim groups share one line).
-//   Measured: gate/up of one token, two experts of 3584 x 4096, palette, 20 us
-// for 90 MB, the read rate but for 5 us of launch and first loads; 1024 x 4096
-// 5.7 us, nothing but those.
+//   Measured: gate/up of one token, two experts of 3584 x 4096, palette, 17.7 us
+// for 90 MB, the read rate but for 3 us of launch and first loads; 1024 x 4096
+// 5.4 us, nothing but those; bf16, one row of 14336 x 4096, 19.7 us for 117 MB.
 #include "grouped_common.h"
 #include "kernels.h"
 
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void gemv_rows_kernel(GroupArgs a,
 // A wave owns an output row and walks that row of every chosen expert's matrix
 // in turn, so the sum stays in its registers: no array of the experts' outputs
 // and no launch that adds it (a layer of one token, two of 8 experts of 3584 x
-// 4096, palette: 35.5 us, 38.1 with a launch for each).  Items, ring and rebuild
+// 4096, palette: 32.4 us; with a launch for each 2.6 more).  Items, ring and rebuild
 // as above; lane j*tiles + i keeps the verbatim word and base of tile i of expert j's row.
 template <bool PAL, int D>
 __global__ __launch_bounds__(64 * kGemvWaves) void gemv_combine_kernel(GroupArgs a, CombineArgs c) {

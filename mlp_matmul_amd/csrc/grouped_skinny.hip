@@ -20,8 +20,8 @@
 // of 4096 columns (at most two tiles of 64 groups); longer K-slices run one
 // segment after another.  A last step of 64 columns multiplies zeros by zeros
 // in its upper half.
-//   Measured: gate/up of 33 tokens, 16 experts of 1792 x 4096 in bf16, 83 us for
-// 470 MB (5.7 TB/s); 16 rows of 4096 x 14336, palette, 24 us for 91 MB, 8 of
+//   Measured: gate/up of 33 tokens, 16 experts of 1792 x 4096 in bf16, 87 us for
+// 470 MB (5.4 TB/s); 16 rows of 4096 x 14336, palette, 22 us for 91 MB, 6 of
 // them the launch, the first loads and the last sums.
 #include <algorithm>
 

@@ -5,8 +5,8 @@
 // columns.  Both tiles go from memory to LDS by global_load_lds, S steps of
 // them there or on their way.  A wave owns a (MT/WM) x (NT/2) block of the
 // output: 64 x 64 with 256 x 128 tiles and eight waves, 16 fragments of 1 KB
-// from LDS for 64 MFMAs of 16 cycles: the LDS and the matrix units are equally
-// busy; 64 x 128 with 256 x 256, three quarters of the LDS's time.  Fragments
+// from LDS for 32 MFMAs of 16 cycles a step; 64 x 128 with 256 x 256, 24 for 64:
+// three quarters of the LDS reads an MFMA.  Fragments
 // of the next 32 columns are read into a second register set while the MFMAs
 // of these run.  One barrier a step, in its middle: by then every wave has the
 // step's last fragments in registers and its own loads of the next step have

@@ -11,7 +11,8 @@
 // time.  One half of a step's rebuild runs under the MFMAs of each half step.
 //   Bound by the vector instructions of the rebuild and the LDS traffic next to
 // the MFMAs: 8192 x 8192 x 8192 in 1.60 ms (690 TFLOP/s) with 128 x 128 tiles;
-// 192 or 256 weight rows, 12 waves or a deeper ring were no faster.
+// 192 or 256 weight rows, 12 waves or a deeper ring were no faster: none of them
+// changes the rebuild's share of an MFMA, which more input rows a tile would.
 #include "grouped_common.h"
 #include "kernels.h"
 
