@@ -525,6 +525,95 @@ int uw_moe_layer(const uint16_t* gate_w, const uw_dmat* gate_d, const uint16_t* 
 int64_t uw_moe_scratch_bytes(int compressed, int64_t tokens, int experts, int top_k, int64_t rows,
                              int64_t cols);
 
+/* The router's selection by scores.  A token's score of expert i is
+ *   s_i = 1 / (1 + exp(-l_i))  or  exp(l_i - max) / sum exp(l_k - max),
+ * rounded to fp32 once (UW_SCORE_SIGMOID, UW_SCORE_SOFTMAX), and its key is
+ * k_i = s_i + bias[i] in fp32 (bias fp32 [experts], NULL: 0): the bias counts for
+ * the choice alone.  The experts form `groups` groups of experts/groups neighbours; a
+ * group's key is the sum of its group_top (1 or 2) largest keys in fp32 (of the
+ * one, where only one expert can be chosen), and the experts of the top_groups
+ * largest groups are considered.  Of them the top_k largest keys are chosen.
+ * Equal keys, of groups and of experts, go by the lowest index.
+ *   ids[t][j]     the expert of the j-th largest key
+ *   weights[t][j] scale * s, or scale * s / (the sum of the chosen s) with
+ *                 renormalize; 0 where that sum is 0
+ * offsets, order, place, the logits' types and strides, -inf and NaN logits, tokens
+ * with fewer experts than top_k, limits, scratch and its size as in
+ * uw_moe_route; an expert whose bias is -inf or NaN is never chosen.  groups
+ * 1..16; the chosen groups hold at least top_k experts. */
+enum { UW_SCORE_SIGMOID = 1, UW_SCORE_SOFTMAX = 2 };
+int uw_moe_route_scored(const void* logits, int logits_type, int64_t ld, int64_t tokens, int experts,
+                        int top_k, int score, const float* bias, int groups, int top_groups,
+                        int group_top, int renormalize, float scale, int32_t* ids, float* weights,
+                        int32_t* offsets, int32_t* order, int32_t* place, void* scratch,
+                        uint64_t scratch_bytes, void* stream);
+
+/* ------------------------------------------------- microscaled 4-bit numbers */
+/* Weights and activations in the 4-bit microscaling format of the Open Compute
+ * Project's MX specification (the pages define none of it: API).  The 32 numbers
+ * of columns 32b .. 32b+31 of a row share the scale 2^(s - 127), s an unsigned byte
+ * (255: every number of the block is NaN); each is a code of four bits times
+ * it, 0-7: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and 8-15: their negatives.  Products of
+ * codes and scales with bf16 or other 4-bit numbers are exact in fp32 (but for
+ * their range) and are added in fp32.
+ *   codes   [rows, cols/2] bytes, the even column in the low half
+ *   scales  [rows, cols/32] bytes
+ * cols is a multiple of 32; rows lie ldc and lds bytes apart, multiples of 16.
+ * Kernels may read, and ignore, the bytes of the 16-byte unit in which a row of
+ * scales ends.  Rows of one expert's matrix span less than 2^31 bytes. */
+typedef struct {
+    int64_t rows, cols;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int64_t ldc, lds;
+} uw_mx4;
+
+/* X (bf16, or fp32 with a row stride that is a multiple of 4) to codes and
+ * scales.  With m the largest magnitude of a block, 2^(s-127) =
+ * 2^(floor(log2 m) - 2), s at least 0; numbers are rounded to the nearest code,
+ * ties to the even one, magnitudes that round above 6 to 6 (they are below 8).  A
+ * block with a NaN or an infinity gets s = 255 and codes 0. */
+int uw_mx4_quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t cols, uint8_t* codes,
+                    int64_t ldc, uint8_t* scales, int64_t lds, void* stream);
+
+/* The numbers themselves, fp32 or bf16 (both hold every one below 2^128). */
+int uw_mx4_dequantize(const uw_mx4* m, void* out, int out_type, int64_t ldo, void* stream);
+
+/* uw_linear, uw_gemm_grouped and uw_moe_gate_up with 4-bit weights w, gate and up
+ * (experts: [experts*rows, cols]).  The rows that are multiplied are bf16 X, as
+ * there, or 4-bit x4 (rows as X's), the other NULL; 4-bit ones run on the matrix
+ * units' 4-bit instructions.  Everything else as there; no scratch. */
+int uw_mx4_linear(const uw_mx4* w, const uint16_t* X, int64_t ldx, const uw_mx4* x4, int64_t batch,
+                  const void* bias, int bias_type, int act,
+                  const void* residual, int residual_type, int64_t ldr,
+                  void* out, int out_type, int64_t ldo, void* stream);
+int uw_mx4_gemm_grouped(const uw_mx4* w, int experts, const uint16_t* X, int64_t x_rows, int64_t ldx,
+                        const uw_mx4* x4, const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
+                        void* out, int out_type, int64_t ldo, void* stream);
+int uw_mx4_gate_up(const uw_mx4* gate, const uw_mx4* up, int experts,
+                   const uint16_t* X, int64_t x_rows, int64_t ldx, const uw_mx4* x4,
+                   const int32_t* offsets, const int32_t* order, int top_k, int64_t n,
+                   uint16_t* h, int64_t ldh, void* stream);
+
+/* uw_moe_layer behind a routing that either router made: gate/up, down on the
+ * bf16 h, and the weighted sum, out[t] = sum_j weights[t][j] down_e(h_tj) +
+ * residual[t].  gate, up, down: bf16 matrices, uw_dmat or uw_mx4, by `form`; of
+ * uw_mx4 rows and cols are multiples of 32.  offsets, order and place as the
+ * routers return them for tokens * top_k slots; out may be X or the residual.
+ * scratch: uw_moe_experts_scratch_bytes() bytes (with UW_FORM_COMPRESSED those
+ * that UW_FORM_BF16 asks for do too, see uw_gemm_grouped); calls that share it
+ * must be ordered. */
+enum { UW_FORM_BF16 = 0, UW_FORM_COMPRESSED = 1, UW_FORM_MX4 = 2 };
+int uw_moe_experts(int form, const void* gate, const void* up, const void* down,
+                   int experts, int64_t rows, int64_t cols,
+                   const uint16_t* X, int64_t ldx, int64_t tokens, int top_k, const float* weights,
+                   const int32_t* offsets, const int32_t* order, const int32_t* place,
+                   const void* residual, int residual_type, int64_t ldr,
+                   void* out, int out_type, int64_t ldo,
+                   void* scratch, uint64_t scratch_bytes, void* stream);
+int64_t uw_moe_experts_scratch_bytes(int form, int64_t tokens, int experts, int top_k, int64_t rows,
+                                     int64_t cols);
+
 /* ----------------------------------------------------------- kernel timer */
 /* (API) Per-launch durations of the matmul kernels (GEMV and MFMA), for measuring
  * them on their own stream.  While enabled, each matmul kernel launch takes

@@ -22,14 +22,16 @@ from ._capi import (  # noqa: F401
     UW_PIPE_AUTO, UW_PIPE_BF16, UW_PIPE_DIRECT, UW_PIPE_EXP, UW_PIPE_FULL, UW_PIPE_HUFF, UW_PIPE_PAL,
     UW_SEC_BITMAP, UW_SEC_DLUT, UW_SEC_GLEN, UW_SEC_MLUT, UW_SEC_NIB, UW_SEC_SM, UW_SEC_STREAM,
     UW_SEC_TILE_OFF, UW_SEC_TILE_VBASE, UW_SEC_VEXP, UW_EUNSUPPORTED, UW_EINVAL, UW_STATIC_SCRATCH_BYTES,
+    UW_FORM_BF16, UW_FORM_COMPRESSED, UW_FORM_MX4, UW_SCORE_SIGMOID, UW_SCORE_SOFTMAX,
     UnweightError, check, lib,
-    uw_dmat, uw_info,
+    uw_dmat, uw_info, uw_mx4,
     uw_opts,
 )
 
 PIPELINES = {"full": UW_PIPE_FULL, "exp": UW_PIPE_EXP, "pal": UW_PIPE_PAL, "direct": UW_PIPE_DIRECT}
 ACTIVATIONS = {"none": UW_ACT_NONE, "relu": UW_ACT_RELU, "silu": UW_ACT_SILU, "gelu": UW_ACT_GELU,
                "gelu_tanh": UW_ACT_GELU_TANH}
+SCORES = {"sigmoid": UW_SCORE_SIGMOID, "softmax": UW_SCORE_SOFTMAX}
 KERNELS = {"auto": UW_KERNEL_AUTO, "gemv": UW_KERNEL_GEMV, "mfma": UW_KERNEL_MFMA, "skinny": UW_KERNEL_SKINNY}
 
 # sections each use reads on the device
@@ -202,6 +204,42 @@ class DeviceMatrix:
         return sum(int(self.info.section_bytes[SECTION_NAMES.index(n)]) for n in self.buffers)
 
 
+class Mx4Matrix:
+    """A matrix of microscaled 4-bit numbers on the device (uw_mx4): codes uint8
+    [rows, cols/2] and scales uint8 [rows, cols/32], the rows of each contiguous
+    and a multiple of 16 bytes apart.  The matrices of a layer's experts are one
+    matrix of experts*rows rows.  The tensors are kept, not copied; their addresses are
+    taken once, so they are not to be resized or moved."""
+
+    requires_grad = False              # as a tensor's
+
+    def __init__(self, codes, scales):
+        torch = _torch()
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if t.dtype != torch.uint8 or t.dim() != 2:
+                raise ValueError(f"{name} must be a 2-D uint8 tensor")
+            if t.shape[1] > 1 and t.stride(1) != 1:
+                raise ValueError(f"the rows of {name} must be contiguous")
+            if t.shape[0] > 1 and t.stride(0) % 16 or t.data_ptr() % 16:
+                raise ValueError(f"the rows of {name} must lie at multiples of 16 bytes")
+        if scales.shape[0] != codes.shape[0] or codes.shape[1] != 16 * scales.shape[1]:
+            raise ValueError(f"codes [rows, cols/2] and scales [rows, cols/32] do not match: {list(codes.shape)}, "
+                             f"{list(scales.shape)}")
+        if codes.device != scales.device:
+            raise ValueError(f"codes on {codes.device} and scales on {scales.device}")
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.rows, self.cols = codes.shape[0], codes.shape[1] * 2
+        self.shape = (self.rows, self.cols)
+
+        def stride(t):
+            return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+        self.mx4 = uw_mx4(self.rows, self.cols, codes.data_ptr(), scales.data_ptr(), stride(codes), stride(scales))
+
+    def device_bytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+
 # ---------------------------------------------------------------- operations
 def decode_full(dm: DeviceMatrix, out=None, stream=None):
     torch = _torch()
@@ -349,8 +387,9 @@ def silu_mul_bf16(g, u, h=None, stream=None):
 
 
 # ------------------------------- matmul with an epilogue, mixture of experts
-# A weight is a contiguous bf16 tensor or a DeviceMatrix with the sections of
-# the direct-palette form.  Tensors of a call are on one device, which need
+# A weight is a contiguous bf16 tensor, a DeviceMatrix with the sections of the
+# direct-palette form, or an Mx4Matrix, whose products take an Mx4Matrix of the
+# same format as X too.  Tensors of a call are on one device, which need
 # not be the current one; the call runs on that device's current stream, or on
 # `stream` (a raw handle), where its outputs are allocated too.  There is no
 # backward pass: tensors that require a gradient are refused outside
@@ -391,6 +430,25 @@ def _x_arg(X, cols=None):
     return ld if X.shape[0] > 1 else (X.shape[1] + 7) // 8 * 8
 
 
+def _mx4_rows(X, cols):
+    """(bf16 pointer, row stride, descriptor, rows) of what 4-bit weights are multiplied with."""
+    if isinstance(X, Mx4Matrix):
+        if X.cols != cols:
+            raise ValueError(f"X must be [rows, {cols}], not {list(X.shape)}")
+        return None, 0, ct.byref(X.mx4), X.rows
+    ld = _x_arg(X, cols)
+    return X.data_ptr(), ld, None, X.shape[0]
+
+
+def _mx4_weight(W, experts, name="W"):
+    """Rows of one expert's matrix."""
+    if not isinstance(W, Mx4Matrix):
+        raise ValueError(f"{name} must be an Mx4Matrix as the other weights are")
+    if W.rows % experts:
+        raise ValueError(f"{name}: {W.rows} rows are not {experts} experts' matrices")
+    return W.rows // experts
+
+
 def _index_arg(t, name, shape):
     if t.dtype != _torch().int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)}")
@@ -398,6 +456,8 @@ def _index_arg(t, name, shape):
 
 def _weight_arg(W, experts, name="W"):
     """(bf16 pointer, descriptor, rows, cols) of one expert's matrix."""
+    if isinstance(W, Mx4Matrix):
+        raise ValueError(f"{name} is an Mx4Matrix: the other weights must be too")
     if isinstance(W, DeviceMatrix):
         n = experts or 1
         if W.rows % n:
@@ -497,7 +557,8 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     may be the residual itself.  `scratch` (None: allocated where it helps) is a
     tensor of any size: for large batches of compressed weights it holds the
     matrix as bf16 (2 bytes a weight), sums of K-slices for others; an empty one
-    saves that memory and is slower."""
+    saves that memory and is slower.  With an Mx4Matrix W (uw_mx4_linear) X may be
+    one too, and no scratch is taken."""
     dev = _one_device(X, W, bias, residual, out, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -505,12 +566,22 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
             return linear(W, X, bias, act, residual, out, out_dtype, scratch)
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
-    w, d, rows, cols = _weight_arg(W, None)
-    ldx, batch = _x_arg(X, cols), X.shape[0]
+    mx4 = isinstance(W, Mx4Matrix)
+    if mx4:
+        rows, cols = W.rows, W.cols
+        xp, ldx, x4, batch = _mx4_rows(X, cols)
+    else:
+        w, d, rows, cols = _weight_arg(W, None)
+        ldx, batch = _x_arg(X, cols), X.shape[0]
     if bias is not None and (bias.dim() != 1 or bias.shape[0] != rows or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous [{rows}] tensor")
     res, res_type, ldr = _residual_arg(residual, batch, rows)
     out, ldo, out_type = _out_arg(out, batch, rows, out_dtype, dev)
+    if mx4:
+        check(lib().uw_mx4_linear(ct.byref(W.mx4), xp, ldx, x4, batch, None if bias is None else bias.data_ptr(),
+                                  UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type,
+                                  ldr, out.data_ptr(), out_type, ldo, _current_stream(dev)), "uw_mx4_linear")
+        return out
     if scratch is None and batch > 2:                        # never any through 2 rows
         need = lib().uw_linear_scratch_bytes(0 if d is None else 1, rows, cols, batch)
         scratch = _new_scratch(need, 0, dev)
@@ -521,6 +592,21 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     return out
 
 
+def _routing(tokens, experts, top_k, scratch, dev):
+    """(a Routing's tensors, the scratch that a routing call needs)"""
+    torch = _torch()
+    need = lib().uw_moe_route_scratch_bytes(tokens, experts, top_k)
+    if need < 0:
+        check(int(need), "uw_moe_route")
+    if scratch is None and need:
+        scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    i32 = torch.int32
+    return Routing(_new_matrix(tokens, top_k, i32, dev), _new_matrix(tokens, top_k, torch.float32, dev),
+                   torch.empty_strided((experts + 1,), (1,), dtype=i32, device=dev),
+                   torch.empty_strided((tokens * top_k,), (1,), dtype=i32, device=dev),
+                   _new_matrix(tokens, top_k, i32, dev)), scratch
+
+
 def moe_route(logits, top_k, renormalize=True, scratch=None, stream=None) -> Routing:
     """uw_moe_route: the top_k experts of every token (logits [tokens, experts],
     fp32 or bf16), their softmax weights, and the slots grouped by expert."""
@@ -529,23 +615,43 @@ def moe_route(logits, top_k, renormalize=True, scratch=None, stream=None) -> Rou
     if ctx is not None:
         with ctx:
             return moe_route(logits, top_k, renormalize, scratch)
-    torch = _torch()
     ld, kind = _matrix_arg(logits, "logits"), _value_type(logits, "logits")
     tokens, experts = logits.shape
-    need = lib().uw_moe_route_scratch_bytes(tokens, experts, top_k)
-    if need < 0:
-        check(int(need), "uw_moe_route")
-    if scratch is None and need:
-        scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-    i32 = torch.int32
-    r = Routing(_new_matrix(tokens, top_k, i32, dev), _new_matrix(tokens, top_k, torch.float32, dev),
-                torch.empty_strided((experts + 1,), (1,), dtype=i32, device=dev),
-                torch.empty_strided((tokens * top_k,), (1,), dtype=i32, device=dev),
-                _new_matrix(tokens, top_k, i32, dev))
+    r, scratch = _routing(tokens, experts, top_k, scratch, dev)
     sp, sb = _scratch_arg(scratch)
     check(lib().uw_moe_route(logits.data_ptr(), kind, ld, tokens, experts, top_k, 1 if renormalize else 0,
                              r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.order.data_ptr(),
                              r.place.data_ptr(), sp, sb, _current_stream(dev)), "uw_moe_route")
+    return r
+
+
+def moe_route_scored(logits, top_k, score="sigmoid", bias=None, groups=1, top_groups=1, group_top=2, renormalize=True,
+                     scale=1.0, scratch=None, stream=None) -> Routing:
+    """uw_moe_route_scored: the top_k experts of every token by their scores
+    ("sigmoid" or "softmax" of logits [tokens, experts], fp32 or bf16) plus
+    `bias` (fp32 [experts], for the choice alone), among the experts of the
+    top_groups of `groups` groups of neighbours with the largest sums of their
+    group_top best; the weights are the chosen scores, renormalised and scaled.
+    The Routing is moe_route's."""
+    dev = _one_device(logits, bias, scratch)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_route_scored(logits, top_k, score, bias, groups, top_groups, group_top, renormalize, scale, scratch)
+    torch = _torch()
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    ld, kind = _matrix_arg(logits, "logits"), _value_type(logits, "logits")
+    tokens, experts = logits.shape
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (experts,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous float32 [{experts}] tensor")
+    r, scratch = _routing(tokens, experts, top_k, scratch, dev)
+    sp, sb = _scratch_arg(scratch)
+    check(lib().uw_moe_route_scored(logits.data_ptr(), kind, ld, tokens, experts, top_k, SCORES[score],
+                                    None if bias is None else bias.data_ptr(), groups, top_groups, group_top,
+                                    1 if renormalize else 0, scale, r.ids.data_ptr(), r.weights.data_ptr(),
+                                    r.offsets.data_ptr(), r.order.data_ptr(), r.place.data_ptr(), sp, sb,
+                                    _current_stream(dev)), "uw_moe_route_scored")
     return r
 
 
@@ -578,13 +684,22 @@ def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, s
     `scratch` (None: allocated where it helps) is a tensor of any size; for
     compressed weights of experts with hundreds of rows it holds every expert's
     matrix as bf16 (2 bytes a weight; the pair of moe_gate_up both matrices), an
-    empty one saves that memory and is slower."""
+    empty one saves that memory and is slower.  With an Mx4Matrix W
+    (uw_mx4_gemm_grouped) X may be one too, and no scratch is taken."""
     dev = _one_device(X, W, offsets, order, out, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return gemm_grouped(W, X, offsets, order, top_k, out, out_dtype, scratch)
     experts, n = _group_args(X, offsets, order)
+    if isinstance(W, Mx4Matrix):
+        rows = _mx4_weight(W, experts)
+        xp, ldx, x4, x_rows = _mx4_rows(X, W.cols)
+        out, ldo, out_type = _out_arg(out, n, rows, out_dtype, dev)
+        check(lib().uw_mx4_gemm_grouped(ct.byref(W.mx4), experts, xp, x_rows, ldx, x4, offsets.data_ptr(),
+                                        None if order is None else order.data_ptr(), top_k, n, out.data_ptr(), out_type,
+                                        ldo, _current_stream(dev)), "uw_mx4_gemm_grouped")
+        return out
     w, d, rows, cols = _weight_arg(W, experts)
     ldx = _x_arg(X, cols)
     out, ldo, out_type = _out_arg(out, n, rows, out_dtype, dev)
@@ -596,14 +711,25 @@ def gemm_grouped(W, X, offsets, order=None, top_k=1, out=None, out_dtype=None, s
 
 
 def moe_gate_up(gate, up, X, offsets, order=None, top_k=1, h=None, scratch=None, stream=None):
-    """uw_moe_gate_up: h = bf16(SiLU(x . gate_e^T) * (x . up_e^T)), rows,
-    inputs and scratch as gemm_grouped's."""
+    """uw_moe_gate_up (uw_mx4_gate_up): h = bf16(SiLU(x . gate_e^T) * (x . up_e^T)),
+    rows, inputs and scratch as gemm_grouped's."""
     dev = _one_device(X, gate, up, offsets, order, h, scratch)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return moe_gate_up(gate, up, X, offsets, order, top_k, h, scratch)
     experts, n = _group_args(X, offsets, order)
+    if isinstance(gate, Mx4Matrix):
+        rows = _mx4_weight(gate, experts, "gate")
+        _mx4_weight(up, experts, "up")
+        if up.shape != gate.shape:
+            raise ValueError("gate and up must have the same shape")
+        xp, ldx, x4, x_rows = _mx4_rows(X, gate.cols)
+        h, ldh, kind = _out_arg(h, n, rows, _torch().bfloat16, dev)
+        check(lib().uw_mx4_gate_up(ct.byref(gate.mx4), ct.byref(up.mx4), experts, xp, x_rows, ldx, x4,
+                                   offsets.data_ptr(), None if order is None else order.data_ptr(), top_k, n,
+                                   h.data_ptr(), ldh, _current_stream(dev)), "uw_mx4_gate_up")
+        return h
     gw, gd, rows, cols = _weight_arg(gate, experts, "gate")
     uw_, ud, urows, ucols = _weight_arg(up, experts, "up")
     if (urows, ucols) != (rows, cols):
@@ -680,6 +806,102 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     check(lib().uw_moe_layer(gw, gd, uw_, ud, dw, dd, experts, F, H, X.data_ptr(), ldx, tokens, logits.data_ptr(), kind,
                              ldl, top_k, 1 if renormalize else 0, res, res_type, ldr, out.data_ptr(), out_type, ldo,
                              sp, sb, _current_stream(dev)), "uw_moe_layer")
+    return out
+
+
+def moe_experts_scratch_bytes(form, tokens, experts, top_k, rows, cols) -> int:
+    n = lib().uw_moe_experts_scratch_bytes(form, tokens, experts, top_k, rows, cols)
+    if n < 0:
+        check(int(n), "uw_moe_experts_scratch_bytes")
+    return int(n)
+
+
+def moe_experts(gate, up, down, X, routing, residual=None, out=None, out_dtype=None, scratch=None, stream=None):
+    """uw_moe_experts: moe_layer's sum over each token's experts (+ residual) on
+    a Routing that moe_route or moe_route_scored returned.  gate, up and down as
+    moe_layer's, or all three Mx4Matrix of experts*F, experts*F and experts*H
+    rows; `out` may be X or the residual.  `scratch` (None: allocated) needs
+    moe_experts_scratch_bytes() bytes; for DeviceMatrix weights those of
+    UW_FORM_BF16 do too, and prompts are slower."""
+    ids, weights, offsets, order, place = routing
+    dev = _one_device(X, gate, up, down, weights, offsets, order, place, residual, out, scratch)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return moe_experts(gate, up, down, X, routing, residual, out, out_dtype, scratch)
+    if place.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("place must be [tokens, top_k] and offsets [experts + 1]")
+    (tokens, top_k), experts = place.shape, offsets.shape[0] - 1
+    _index_arg(place, "place", (X.shape[0], top_k))
+    _index_arg(order, "order", (tokens * top_k,))
+    _index_arg(offsets, "offsets", (experts + 1,))
+    if weights.dtype != _torch().float32 or weights.shape != place.shape or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 tensor of place's shape")
+    least_form = UW_FORM_BF16
+    if isinstance(gate, Mx4Matrix):
+        form = least_form = UW_FORM_MX4
+        F, H = _mx4_weight(gate, experts, "gate"), gate.cols
+        shapes = (_mx4_weight(up, experts, "up"), up.cols), (_mx4_weight(down, experts, "down"), down.cols)
+        ws = [ct.byref(m.mx4) for m in (gate, up, down)]
+    else:
+        parts = [_weight_arg(m, experts, name) for m, name in ((gate, "gate"), (up, "up"), (down, "down"))]
+        form = UW_FORM_BF16 if parts[0][1] is None else UW_FORM_COMPRESSED
+        if any((p[1] is None) != (parts[0][1] is None) for p in parts):
+            raise ValueError("gate, up and down must be of one form")
+        F, H = parts[0][2:]
+        shapes = parts[1][2:], parts[2][2:]
+        ws = [p[0] if p[1] is None else p[1] for p in parts]
+    if shapes != ((F, H), (H, F)):
+        raise ValueError("gate and up must be [experts, F, H] and down [experts, H, F]")
+    ldx = _x_arg(X, H)
+    res, res_type, ldr = _residual_arg(residual, tokens, H)
+    out, ldo, out_type = _out_arg(out, tokens, H, out_dtype, dev)
+    if scratch is None:
+        need = moe_experts_scratch_bytes(form, tokens, experts, top_k, F, H)
+        least = need if form == least_form else moe_experts_scratch_bytes(least_form, tokens, experts, top_k, F, H)
+        scratch = _new_scratch(need, least, dev)
+    sp, sb = _scratch_arg(scratch)
+    check(lib().uw_moe_experts(form, *ws, experts, F, H, X.data_ptr(), ldx, tokens, top_k, weights.data_ptr(),
+                               offsets.data_ptr(), order.data_ptr(), place.data_ptr(), res, res_type, ldr,
+                               out.data_ptr(), out_type, ldo, sp, sb, _current_stream(dev)), "uw_moe_experts")
+    return out
+
+
+# ------------------------------------------------- microscaled 4-bit numbers
+def mx4_quantize(X, out=None, stream=None) -> Mx4Matrix:
+    """uw_mx4_quantize: X [rows, cols] (bf16 or fp32, cols a multiple of 32) as
+    microscaled 4-bit numbers, in a new Mx4Matrix or in `out`."""
+    dev = _one_device(X, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return mx4_quantize(X, out)
+    torch = _torch()
+    ld, kind = _matrix_arg(X, "X"), _value_type(X, "X")
+    rows, cols = X.shape
+    if cols % 32:
+        raise ValueError(f"X must have a multiple of 32 columns, not {cols}")
+    if out is None:
+        room = (cols // 32 + 15) // 16 * 16
+        out = Mx4Matrix(torch.empty_strided((rows, cols // 2), (cols // 2, 1), dtype=torch.uint8, device=dev),
+                        torch.empty_strided((rows, cols // 32), (room, 1), dtype=torch.uint8, device=dev))
+    elif out.shape != (rows, cols):
+        raise ValueError(f"out must be [{rows}, {cols}], not {list(out.shape)}")
+    m = out.mx4
+    check(lib().uw_mx4_quantize(X.data_ptr(), kind, ld, rows, cols, m.codes, m.ldc, m.scales, m.lds,
+                                _current_stream(dev)), "uw_mx4_quantize")
+    return out
+
+
+def mx4_dequantize(M: Mx4Matrix, out=None, out_dtype=None, stream=None):
+    """uw_mx4_dequantize: the numbers of M, fp32 by default or bf16."""
+    dev = _one_device(M, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return mx4_dequantize(M, out, out_dtype)
+    out, ldo, kind = _out_arg(out, M.rows, M.cols, out_dtype, dev)
+    check(lib().uw_mx4_dequantize(ct.byref(M.mx4), out.data_ptr(), kind, ldo, _current_stream(dev)), "uw_mx4_dequantize")
     return out
 
 

@@ -23,6 +23,8 @@ UW_KERNEL_AUTO, UW_KERNEL_GEMV, UW_KERNEL_MFMA, UW_KERNEL_SKINNY = 0, 1, 2, 3
 UW_PIPE_AUTO, UW_PIPE_FULL, UW_PIPE_EXP, UW_PIPE_PAL, UW_PIPE_DIRECT, UW_PIPE_BF16, UW_PIPE_HUFF = range(7)
 UW_STATIC_SCRATCH_BYTES = 64 << 20
 UW_F32, UW_BF16 = 0, 1
+UW_SCORE_SIGMOID, UW_SCORE_SOFTMAX = 1, 2
+UW_FORM_BF16, UW_FORM_COMPRESSED, UW_FORM_MX4 = range(3)
 UW_ACT_NONE, UW_ACT_RELU, UW_ACT_SILU, UW_ACT_GELU, UW_ACT_GELU_TANH = range(5)
 
 
@@ -54,10 +56,17 @@ class uw_dmat(ct.Structure):
     ]
 
 
+class uw_mx4(ct.Structure):
+    _fields_ = [("rows", ct.c_int64), ("cols", ct.c_int64), ("codes", ct.c_void_p), ("scales", ct.c_void_p),
+                ("ldc", ct.c_int64), ("lds", ct.c_int64)]
+
+
 _P = ct.c_void_p
+_M = ct.POINTER(uw_mx4)
 _I64 = ct.c_int64
 _U64 = ct.c_uint64
 _INT = ct.c_int
+_FLOAT = ct.c_float
 
 # name -> (restype, argtypes); every function declared in include/unweight.h
 SIGNATURES = {
@@ -101,6 +110,16 @@ SIGNATURES = {
     "uw_moe_layer": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _INT, _I64, _INT, _INT, _P,
                              _INT, _I64, _P, _INT, _I64, _P, _U64, _P]),
     "uw_moe_scratch_bytes": (_I64, [_INT, _I64, _INT, _INT, _I64, _I64]),
+    "uw_moe_route_scored": (_INT, [_P, _INT, _I64, _I64, _INT, _INT, _INT, _P, _INT, _INT, _INT, _INT, _FLOAT, _P, _P,
+                                    _P, _P, _P, _P, _U64, _P]),
+    "uw_mx4_quantize": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "uw_mx4_dequantize": (_INT, [_M, _P, _INT, _I64, _P]),
+    "uw_mx4_linear": (_INT, [_M, _P, _I64, _M, _I64, _P, _INT, _INT, _P, _INT, _I64, _P, _INT, _I64, _P]),
+    "uw_mx4_gemm_grouped": (_INT, [_M, _INT, _P, _I64, _I64, _M, _P, _P, _INT, _I64, _P, _INT, _I64, _P]),
+    "uw_mx4_gate_up": (_INT, [_M, _M, _INT, _P, _I64, _I64, _M, _P, _P, _INT, _I64, _P, _I64, _P]),
+    "uw_moe_experts": (_INT, [_INT, _P, _P, _P, _INT, _I64, _I64, _P, _I64, _I64, _INT, _P, _P, _P, _P, _P, _INT, _I64,
+                               _P, _INT, _I64, _P, _U64, _P]),
+    "uw_moe_experts_scratch_bytes": (_I64, [_INT, _I64, _INT, _INT, _I64, _I64]),
     "uw_kernel_timer_enable": (_INT, [_INT]),
     "uw_kernel_timer_disable": (_INT, []),
     "uw_kernel_timer_reset": (_INT, []),

@@ -1,192 +1,11 @@
 // C ABI entry points of the epilogue matmul and of the mixture-of-experts
 // operators: argument checks, scratch layout and composition.  See unweight.h
 // for the contract.
-#include <algorithm>
-#include <exception>
-#include <utility>
+#include "capi_experts.h"
 
-#include "capi_common.h"
-#include "experts.h"
-
-using uw::align256;
-using uw::aligned16;
-using uw::as_stream;
-using uw::fail;
-using uw::hip_fail;
+using namespace uw;
 
 namespace {
-
-// No C++ exception leaves an entry point (the error text itself allocates).
-template <class F>
-int guarded(F&& f) noexcept {
-    try {
-        uw::clear_error();
-        return f();
-    } catch (const std::exception&) {
-        return UW_ENOMEM;
-    }
-}
-
-int bad(const char* who, const char* what) { return fail(UW_EINVAL, std::string(who) + ": " + what); }
-
-bool value_type(int t) { return t == UW_F32 || t == UW_BF16; }
-int64_t value_bytes(int t) { return t == UW_BF16 ? 2 : 4; }
-
-// Bytes from the first to behind the last element of [rows, cols] with row stride ld.
-uint64_t span(int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
-    return rows > 0 && cols > 0 ? (uint64_t(rows - 1) * uint64_t(ld) + uint64_t(cols)) * uint64_t(bytes) : 0;
-}
-
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na && nb && x < y + nb && y < x + na;
-}
-
-// Memory that a call reads (or writes).
-struct Inputs {
-    struct {
-        const void* p;
-        uint64_t bytes;
-    } span[24];
-    int count = 0;
-
-    void add(const void* p, uint64_t bytes) {
-        if (p && bytes) span[count++] = {p, bytes};
-    }
-    bool meet(const void* p, uint64_t bytes) const {
-        for (int i = 0; i < count; ++i)
-            if (overlap(p, bytes, span[i].p, span[i].bytes)) return true;
-        return false;
-    }
-};
-
-// The weight of an operator: exactly one of w (bf16) and d (compressed, with
-// its NIB section), [experts*rows, cols].
-int take_weight(const uint16_t* w, const uw_dmat* d, int64_t experts, int64_t rows, int64_t cols, uwk::Weight* out,
-                Inputs* in, const char* who) {
-    *out = uwk::Weight{};
-    if (rows < 0 || cols < uw::kGroup || cols % uw::kGroup)
-        return bad(who, "bad shape (cols must be a positive multiple of 64)");
-    if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows * cols >= (int64_t(1) << 31))
-        return fail(UW_EUNSUPPORTED, std::string(who) + ": a matrix of 2^31 weights or more");
-    if (rows == 0 && !d) return UW_OK;
-    if ((w != nullptr) == (d != nullptr)) return bad(who, "give a bf16 weight or a compressed one, and not both");
-    if (w) {
-        if (!aligned16(w)) return bad(who, "misaligned weight");
-        in->add(w, uint64_t(experts * rows * cols) * 2);
-        out->w = w;
-        return UW_OK;
-    }
-    int rc = uw::check_dmat(d, who);
-    if (rc) return rc;
-    if (d->rows != experts * rows || d->cols != cols)
-        return bad(who, "the compressed matrix is not [experts*rows, cols]");
-    if (d->groups && (!d->nib || !d->sm || !d->bitmap || !d->tile_vbase || (d->verbatim_groups && !d->vexp)))
-        return bad(who, "the compressed matrix lacks its NIB/SM/BITMAP/TILE_VBASE/VEXP sections");
-    if (!aligned16(d->nib) || !aligned16(d->sm) || !aligned16(d->vexp) || !aligned16(d->bitmap) ||
-        !aligned16(d->tile_vbase))
-        return bad(who, "misaligned section of the compressed matrix");
-    in->add(d->nib, uint64_t(d->groups) * 32);
-    in->add(d->sm, uint64_t(d->groups) * 64);
-    in->add(d->vexp, uint64_t(d->verbatim_groups) * 64);
-    in->add(d->bitmap, uint64_t(d->tiles) * 8);
-    in->add(d->tile_vbase, uint64_t(d->tiles + 1) * 4);
-    out->w = d->nib;
-    out->sm = d->sm;
-    out->vexp = uw::vexp_of(d) ? d->vexp : d->sm;   // never read as exponents without verbatim groups
-    out->bitmap = d->bitmap;
-    out->tile_vbase = d->tile_vbase;
-    uw::pack_palette(d->palette, out->pal);
-    out->last_slot = d->verbatim_groups ? uint32_t(d->verbatim_groups) - 1 : 0;
-    return UW_OK;
-}
-
-int check_rows(const void* p, int64_t ld, int64_t cols, int64_t multiple, const char* who, const char* name) {
-    if (!p || !aligned16(p)) return fail(UW_EINVAL, std::string(who) + ": NULL or misaligned " + name);
-    if (ld < cols || ld % multiple || ld >= (int64_t(1) << 40))
-        return fail(UW_EINVAL, std::string(who) + ": bad row stride of " + name);
-    return UW_OK;
-}
-
-// out (and the residual it may replace) against what the call reads while out is written.
-int check_epilogue(const uwk::Epilogue& e, int64_t n, int64_t rows, const Inputs& in, const char* who) {
-    if (!value_type(e.out_type) || (e.bias && !value_type(e.bias_type)) || (e.residual && !value_type(e.residual_type)))
-        return bad(who, "a value type is neither UW_F32 nor UW_BF16");
-    if (e.act < 0 || e.act >= uwk::ACT_COUNT) return bad(who, "unknown activation");
-    int rc = check_rows(e.out, e.ldo, rows, 1, who, "out");
-    if (rc) return rc;
-    if (e.residual && (rc = check_rows(e.residual, e.ldr, rows, 1, who, "residual"))) return rc;
-    if (e.bias && !aligned16(e.bias)) return bad(who, "misaligned bias");
-    const uint64_t ob = span(n, rows, e.ldo, value_bytes(e.out_type));
-    if (in.meet(e.out, ob)) return bad(who, "out overlaps an input");
-    if (e.residual && overlap(e.out, ob, e.residual, span(n, rows, e.ldr, value_bytes(e.residual_type))) &&
-        (e.out != e.residual || e.ldo != e.ldr || e.out_type != e.residual_type))
-        return bad(who, "out overlaps the residual without being it");
-    return UW_OK;
-}
-
-// Optional scratch, which no input, residual or output may lie in.
-int check_scratch(const void* scratch, uint64_t* bytes, const uwk::Epilogue& e, int64_t n, int64_t rows,
-                  const Inputs& in, const char* who) {
-    if (!aligned16(scratch)) return bad(who, "misaligned scratch");
-    if (!scratch) *bytes = 0;
-    if (overlap(e.out, span(n, rows, e.ldo, value_bytes(e.out_type)), scratch, *bytes) || in.meet(scratch, *bytes) ||
-        (e.residual && overlap(e.residual, span(n, rows, e.ldr, value_bytes(e.residual_type)), scratch, *bytes)))
-        return bad(who, "the scratch overlaps an input or out");
-    return UW_OK;
-}
-
-int check_groups(int experts, int64_t n, const int32_t* offsets, const int32_t* order, int top_k, int64_t x_rows,
-                 const char* who) {
-    if (experts < 1 || experts > uwk::kMaxExperts) return bad(who, "experts must be 1..512");
-    if (n < 0 || x_rows < 0 || n >= (int64_t(1) << 31) || x_rows >= (int64_t(1) << 31))
-        return bad(who, "bad number of rows");
-    if (top_k < 1) return bad(who, "top_k must be at least 1");
-    if (n == 0) return UW_OK;
-    if (!offsets || !aligned16(offsets) || !aligned16(order)) return bad(who, "NULL or misaligned offsets or order");
-    if (order ? x_rows == 0 : x_rows < n) return bad(who, "X has too few rows");
-    return UW_OK;
-}
-
-// What a grouped call reads beside its weights.
-void add_rows(Inputs* in, const uwk::GroupArgs& a) {
-    in->add(a.X, span(a.x_rows, a.C, a.ldx, 2));
-    in->add(a.offsets, uint64_t(a.E + 1) * 4);
-    in->add(a.order, uint64_t(a.n) * 4);
-}
-
-uwk::GroupArgs group_args(const uint16_t* X, int64_t x_rows, int64_t ldx, const int32_t* offsets, const int32_t* order,
-                          int top_k, int64_t n, int64_t experts, int64_t rows, int64_t cols) {
-    uwk::GroupArgs a{};
-    a.X = X;
-    a.offsets = offsets;
-    a.order = order;
-    a.ldx = ldx;
-    a.x_rows = x_rows;
-    a.n = n;
-    a.E = int32_t(experts);
-    a.R = int32_t(rows);
-    a.C = int32_t(cols);
-    a.div = top_k;
-    a.split = 1;
-    a.cus = uw::device_cus();
-    return a;
-}
-
-// Scratch of a routing call with more than one block of tokens.
-uint64_t route_scratch(int64_t tokens, int64_t experts) {
-    int32_t blocks, per;
-    uwk::route_blocks(tokens, &blocks, &per);
-    return blocks > 1 ? align256(uint64_t(blocks) * uint64_t((experts + 7) / 8) * 16) : 0;
-}
-
-int check_routing(int64_t tokens, int experts, int top_k, const char* who) {
-    if (tokens < 0 || tokens >= (int64_t(1) << 31)) return bad(who, "bad number of tokens");
-    if (experts < 1 || experts > uwk::kMaxExperts) return bad(who, "experts must be 1..512");
-    if (top_k < 1 || top_k > uwk::kMaxTopK || top_k > experts) return bad(who, "top_k must be 1..16 and at most experts");
-    if (tokens * top_k >= (int64_t(1) << 31)) return bad(who, "tokens * top_k must be below 2^31");
-    return UW_OK;
-}
 
 // Scratch of a whole layer.
 struct LayerLayout {
@@ -219,6 +38,38 @@ LayerLayout layer_layout(bool pal, int64_t tokens, int experts, int64_t top_k, i
     l.expand = std::max(uwk::grouped_scratch(pal, true, experts, F, H, int64_t(slots), uw::device_cus()),
                         uwk::grouped_scratch(pal, false, experts, H, F, int64_t(slots), uw::device_cus()));
     return l;
+}
+
+// A routing call: a has everything but its blocks and scratch.
+int route(uwk::RouteArgs a, void* scratch, uint64_t scratch_bytes, void* stream, const char* who) {
+    int rc = check_routing(a.tokens, a.experts, a.top_k, who);
+    if (rc) return rc;
+    if (!value_type(a.type)) return bad(who, "logits are UW_F32 or UW_BF16");
+    if (!a.offsets || !aligned16(a.offsets)) return bad(who, "NULL or misaligned offsets");
+    if (a.tokens) {
+        if ((rc = check_rows(a.logits, a.ld, a.experts, 1, who, "logits"))) return rc;
+        for (const void* p : {static_cast<const void*>(a.ids), static_cast<const void*>(a.weights),
+                              static_cast<const void*>(a.order), static_cast<const void*>(a.place)})
+            if (!p || !aligned16(p)) return bad(who, "NULL or misaligned output");
+    }
+    const uint64_t need = route_scratch(a.tokens, a.experts);
+    if (need && (!scratch || !aligned16(scratch) || scratch_bytes < need))
+        return bad(who, "scratch smaller than uw_moe_route_scratch_bytes()");
+    // every block reads its logits while others write: nothing shares memory
+    const uint64_t slots = uint64_t(a.tokens) * uint64_t(a.top_k) * 4;
+    const std::pair<const void*, uint64_t> writes[] = {
+        {a.ids, slots}, {a.weights, slots}, {a.offsets, uint64_t(a.experts + 1) * 4}, {a.order, slots}, {a.place, slots}, {scratch, need}};
+    Inputs others;
+    others.add(a.logits, span(a.tokens, a.experts, a.ld, value_bytes(a.type)));
+    others.add(a.bias, uint64_t(a.experts) * 4);
+    for (const auto& w : writes) {
+        if (others.meet(w.first, w.second)) return bad(who, "an output or the scratch overlaps another or the logits");
+        others.add(w.first, w.second);
+    }
+    a.counts = static_cast<uint16_t*>(scratch);
+    uwk::route_blocks(a.tokens, &a.blocks, &a.per_block);
+    const hipError_t e = uwk::launch_route(a, as_stream(stream));
+    return e == hipSuccess ? UW_OK : hip_fail(e, who);
 }
 
 }  // namespace
@@ -276,35 +127,28 @@ int uw_moe_route(const void* logits, int logits_type, int64_t ld, int64_t tokens
                  int renormalize, int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
                  void* scratch, uint64_t scratch_bytes, void* stream) {
     return guarded([&]() -> int {
-        const char* who = "uw_moe_route";
-        int rc = check_routing(tokens, experts, top_k, who);
-        if (rc) return rc;
-        if (!value_type(logits_type)) return bad(who, "logits are UW_F32 or UW_BF16");
-        if (!offsets || !aligned16(offsets)) return bad(who, "NULL or misaligned offsets");
-        if (tokens) {
-            if ((rc = check_rows(logits, ld, experts, 1, who, "logits"))) return rc;
-            for (const void* p : {static_cast<const void*>(ids), static_cast<const void*>(weights),
-                                  static_cast<const void*>(order), static_cast<const void*>(place)})
-                if (!p || !aligned16(p)) return bad(who, "NULL or misaligned output");
-        }
-        const uint64_t need = route_scratch(tokens, experts);
-        if (need && (!scratch || !aligned16(scratch) || scratch_bytes < need))
-            return bad(who, "scratch smaller than uw_moe_route_scratch_bytes()");
-        // every block reads its logits while others write: nothing shares memory
-        const uint64_t slots = uint64_t(tokens) * uint64_t(top_k) * 4;
-        const std::pair<const void*, uint64_t> writes[] = {{ids, slots},   {weights, slots}, {offsets, uint64_t(experts + 1) * 4},
-                                                           {order, slots}, {place, slots},   {scratch, need}};
-        Inputs others;
-        others.add(logits, span(tokens, experts, ld, value_bytes(logits_type)));
-        for (const auto& w : writes) {
-            if (others.meet(w.first, w.second)) return bad(who, "an output or the scratch overlaps another or the logits");
-            others.add(w.first, w.second);
-        }
-        uwk::RouteArgs a{logits, ld,  tokens,  logits_type, experts, top_k, renormalize != 0, ids, weights,
-                         offsets, order, place, static_cast<uint16_t*>(scratch), 0, 0};
-        uwk::route_blocks(tokens, &a.blocks, &a.per_block);
-        const hipError_t e = uwk::launch_route(a, as_stream(stream));
-        return e == hipSuccess ? UW_OK : hip_fail(e, who);
+        const uwk::RouteArgs a{logits, ld,  tokens,  logits_type, experts, top_k, renormalize != 0, ids, weights,
+                               offsets, order, place, nullptr, 0, 0, uwk::SCORE_LOGIT, nullptr, 1, 1, 1, 1.f};
+        return route(a, scratch, scratch_bytes, stream, "uw_moe_route");
+    });
+}
+
+int uw_moe_route_scored(const void* logits, int logits_type, int64_t ld, int64_t tokens, int experts, int top_k,
+                        int score, const float* bias, int groups, int top_groups, int group_top, int renormalize,
+                        float scale, int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* place,
+                        void* scratch, uint64_t scratch_bytes, void* stream) {
+    return guarded([&]() -> int {
+        const char* who = "uw_moe_route_scored";
+        if (score != UW_SCORE_SIGMOID && score != UW_SCORE_SOFTMAX) return bad(who, "unknown score");
+        if (groups < 1 || groups > uwk::kMaxGroups || experts < 1 || experts % groups)
+            return bad(who, "groups must be 1..16 and divide experts");
+        if (top_groups < 1 || top_groups > groups) return bad(who, "top_groups must be 1..groups");
+        if (group_top < 1 || group_top > 2) return bad(who, "group_top must be 1 or 2");
+        if (int64_t(top_groups) * (experts / groups) < top_k) return bad(who, "the chosen groups have fewer than top_k experts");
+        if (!aligned16(bias)) return bad(who, "misaligned bias");
+        const uwk::RouteArgs a{logits, ld,  tokens,  logits_type, experts, top_k, renormalize != 0, ids, weights,
+                               offsets, order, place, nullptr, 0, 0, score, bias, groups, top_groups, group_top, scale};
+        return route(a, scratch, scratch_bytes, stream, who);
     });
 }
 

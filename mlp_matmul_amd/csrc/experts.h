@@ -85,6 +85,10 @@ hipError_t launch_tile(bool pair, const GroupArgs& a, TileShape shape, hipStream
 enum PalTileShape { PAL_TILE_64x64, PAL_TILE_128x64, PAL_TILE_128x128, PAL_TILE_SHAPES };
 hipError_t launch_tile_pal(bool pair, const GroupArgs& a, PalTileShape shape, hipStream_t s);
 
+constexpr int kMaxGroups = 16;     // of a scored routing's experts: a lane of a DPP row each
+
+enum Score { SCORE_LOGIT = 0, SCORE_SIGMOID = 1, SCORE_SOFTMAX = 2, SCORE_COUNT = 3 };
+
 struct RouteArgs {
     const void* logits;
     int64_t ld, tokens;
@@ -96,6 +100,11 @@ struct RouteArgs {
     int32_t* place;
     uint16_t* counts;           // [blocks, experts up to 8s] of every block's slots, when blocks > 1
     int32_t blocks, per_block;  // tokens of a block: a multiple of 16
+    // scored routing (score not SCORE_LOGIT)
+    int32_t score;
+    const float* bias;          // [experts] or NULL, added to the scores for the choice alone
+    int32_t groups, top_groups, group_top;
+    float scale;
 };
 
 // Blocks of tokens of a routing call (1: a single launch, no counts).

@@ -103,15 +103,18 @@ inline int64_t group_units(const GroupArgs& a, int nt, int64_t bands) {
     return (a.n / nt + (a.n < a.E ? a.n : a.E)) * bands;
 }
 
-// The X row that sorted row s reads (an index outside X reads its row 0).
-__device__ __forceinline__ const uint16_t* group_x_row(const GroupArgs& a, int64_t s) {
+// The row of X that sorted row s reads (an index outside X reads its row 0).
+__device__ __forceinline__ int64_t group_x_index(const GroupArgs& a, int64_t s) {
     int64_t r = s;
     if (a.order) {
         const int32_t o = a.order[s];
         r = o < 0 ? 0 : int64_t(uint32_t(o) / uint32_t(a.div));
         if (r >= a.x_rows) r = 0;
     }
-    return a.X + r * a.ldx;
+    return r;
+}
+__device__ __forceinline__ const uint16_t* group_x_row(const GroupArgs& a, int64_t s) {
+    return a.X + group_x_index(a, s) * a.ldx;
 }
 
 // 16 bytes a lane from memory to LDS; lane i's land at dst + 16 i.
@@ -177,6 +180,7 @@ __device__ __forceinline__ void activate_all(f32x4_t (&v)[N], int act) {
 // multiple of the element.
 typedef uint32_t u32x2_e2_t __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_e4_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_e2_t __attribute__((ext_vector_type(4), aligned(2)));
 
 // Four values of rows r .. r+3 from p[o..], of either type; those from R on are 0.
 __device__ __forceinline__ f32x4_t load4(const void* p, int type, int64_t o, int r, int R) {

@@ -28,6 +28,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "grouped_common.h"
 
@@ -73,69 +74,72 @@ __device__ __forceinline__ float order_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// Selects the experts of tokens t (one per DPP row; t >= tokens: nothing) and
-// counts them in cnt[expert].  V logits a lane, in runs of four where V allows
-// a wide load.
+// The expert that a lane's value c is: runs of four where V allows a wide load.
 template <int V>
-__device__ void select(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt) {
+__device__ __forceinline__ uint32_t expert_of(int c, uint32_t sub) {
     constexpr int W = V < 4 ? 1 : 4;
-    const bool live = t < a.tokens;
-    auto expert = [&](int c) { return uint32_t(16 * W * (c / W) + c % W) + W * sub; };
-    uint32_t key[V];
-    // every load stays inside the logits and none waits for another
-    float f[V];
+    return uint32_t(16 * W * (c / W) + c % W) + W * sub;
+}
+
+// The logits of token t (one per DPP row), V a lane.  Every load stays inside
+// the logits and none waits for another.
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, uint32_t sub, float (&f)[V]) {
+    constexpr int W = V < 4 ? 1 : 4;
     const int E = a.experts;
     const int64_t row = min(t, a.tokens - 1) * a.ld;
     const float* const pf = static_cast<const float*>(a.logits) + row;
     const uint16_t* const ph = static_cast<const uint16_t*>(a.logits) + row;
+    auto expert = [&](int c) { return int(expert_of<V>(c, sub)); };
     if (W == 4 && ((a.ld | E) & 3) == 0 && (reinterpret_cast<uint64_t>(a.logits) & 15) == 0) {
         if (a.type == VT_F32) {
 #pragma unroll
             for (int c = 0; c + W <= V; c += W) {
-                const f32x4_t q = *reinterpret_cast<const f32x4_t*>(pf + min(int(expert(c)), E - W));
+                const f32x4_t q = *reinterpret_cast<const f32x4_t*>(pf + min(expert(c), E - W));
 #pragma unroll
                 for (int k = 0; k < W; ++k) f[c + k] = q[k];
             }
         } else {
 #pragma unroll
             for (int c = 0; c + W <= V; c += W) {
-                const u32x2_t q = *reinterpret_cast<const u32x2_t*>(ph + min(int(expert(c)), E - W));
+                const u32x2_t q = *reinterpret_cast<const u32x2_t*>(ph + min(expert(c), E - W));
 #pragma unroll
                 for (int k = 0; k < W; ++k) f[c + k] = __uint_as_float(k & 1 ? q[k / 2] & 0xFFFF0000u : q[k / 2] << 16);
             }
         }
     } else if (a.type == VT_F32) {
 #pragma unroll
-        for (int c = 0; c < V; ++c) f[c] = pf[min(int(expert(c)), E - 1)];
+        for (int c = 0; c < V; ++c) f[c] = pf[min(expert(c), E - 1)];
     } else {
 #pragma unroll
-        for (int c = 0; c < V; ++c) f[c] = bf16_value(ph[min(int(expert(c)), E - 1)]);
+        for (int c = 0; c < V; ++c) f[c] = bf16_value(ph[min(expert(c), E - 1)]);
     }
+}
+
+template <int V>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[V]) {
+    uint32_t m = key[0];
 #pragma unroll
-    for (int c = 0; c < V; ++c)
-        key[c] = live && int(expert(c)) < E && f[c] > -INFINITY ? order_key(fminf(f[c], FLT_MAX)) : 0;
-    auto largest = [&]() {
-        uint32_t m = key[0];
-#pragma unroll
-        for (int c = 1; c < V; ++c) m = max(m, key[c]);
-        return row_max(m);
-    };
-    float sum = 0.f;
-    if (!a.renorm) {
-        const float top = order_value(largest());
-#pragma unroll
-        for (int c = 0; c < V; ++c) sum += key[c] ? expf(order_value(key[c]) - top) : 0.f;
-        sum = row_sum(sum);
-    }
-    uint32_t my_key = 0, my_id = ~0u, top = 0;
-    for (int j = 0; j < a.top_k; ++j) {
-        const uint32_t m = largest(), find = max(m, 1u);   // 1 is a NaN's key: with m = 0 nothing is found
+    for (int c = 1; c < V; ++c) m = max(m, key[c]);
+    return row_max(m);
+}
+
+struct Choice {
+    uint32_t key, id, top;   // lane j's: those of the j-th chosen; the first one's key
+};
+
+// The top_k largest keys, equal ones by the lowest index; taken ones become 0.
+template <int V>
+__device__ __forceinline__ Choice choose(uint32_t (&key)[V], int top_k, uint32_t sub) {
+    Choice r{0, ~0u, 0};
+    for (int j = 0; j < top_k; ++j) {
+        const uint32_t m = largest(key), find = max(m, 1u);   // 1 is a NaN's key: with m = 0 nothing is found
         bool has[V];
         uint32_t at = ~0u;
 #pragma unroll
         for (int c = V - 1; c >= 0; --c) {
             has[c] = key[c] == find;
-            at = has[c] ? expert(c) : at;
+            at = has[c] ? expert_of<V>(c, sub) : at;
         }
         const uint32_t e = row_min(at);
         bool open = m && at == e;                          // this lane has it: its lowest one goes
@@ -144,19 +148,134 @@ __device__ void select(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cn
             key[c] = has[c] && open ? 0 : key[c];
             open = open && !has[c];
         }
-        top = j == 0 ? m : top;
+        r.top = j == 0 ? m : r.top;
         if (uint32_t(j) == sub) {
-            my_key = m;
-            my_id = e;
+            r.key = m;
+            r.id = e;
         }
     }
-    float w = my_key ? expf(order_value(my_key) - order_value(top)) : 0.f;
+    return r;
+}
+
+// Selects the experts of tokens t (one per DPP row; t >= tokens: nothing) and
+// counts them in cnt[expert].
+template <int V>
+__device__ void select(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt) {
+    const bool live = t < a.tokens;
+    uint32_t key[V];
+    float f[V];
+    load_logits<V>(a, t, sub, f);
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+        key[c] = live && int(expert_of<V>(c, sub)) < a.experts && f[c] > -INFINITY ? order_key(fminf(f[c], FLT_MAX)) : 0;
+    float sum = 0.f;
+    if (!a.renorm) {
+        const float top = order_value(largest(key));
+#pragma unroll
+        for (int c = 0; c < V; ++c) sum += key[c] ? expf(order_value(key[c]) - top) : 0.f;
+        sum = row_sum(sum);
+    }
+    const Choice r = choose<V>(key, a.top_k, sub);
+    const float w = r.key ? expf(order_value(r.key) - order_value(r.top)) : 0.f;
     if (a.renorm) sum = row_sum(w);
     if (live && int(sub) < a.top_k) {
         const int64_t o = t * a.top_k + sub;
-        a.ids[o] = int32_t(my_id);
-        a.weights[o] = my_key ? w / sum : 0.f;
-        if (my_key) atomicAdd(cnt + my_id, 1u);
+        a.ids[o] = int32_t(r.id);
+        a.weights[o] = r.key ? w / sum : 0.f;
+        if (r.key) atomicAdd(cnt + r.id, 1u);
+    }
+}
+
+// Scores decide here, and two of them may be next to each other: they are
+// computed in 64 bits and rounded to fp32 once, so that equal scores are those
+// that are equal after that rounding.
+__device__ __forceinline__ double row_sum64(double v) {
+    auto ror = [](double x, auto n) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const uint64_t lo = row_ror<decltype(n)::value>(uint32_t(b)), hi = row_ror<decltype(n)::value>(uint32_t(b >> 32));
+        return __builtin_bit_cast(double, lo | (hi << 32));
+    };
+    v += ror(v, std::integral_constant<int, 8>{});
+    v += ror(v, std::integral_constant<int, 4>{});
+    v += ror(v, std::integral_constant<int, 2>{});
+    return v + ror(v, std::integral_constant<int, 1>{});
+}
+
+// The score of a finite logit; top and sum: of the token's softmax.
+__device__ __forceinline__ float score_of(const RouteArgs& a, float l, float top, double sum) {
+    if (a.score == SCORE_SIGMOID) return float(1.0 / (1.0 + exp(-double(l))));
+    return float(exp(double(l) - double(top)) / sum);
+}
+
+// select by scores: key = score + bias, groups of experts by their best keys,
+// then the best keys of the chosen groups.  The weights are the scores.
+template <int V>
+__device__ void select_scored(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt) {
+    const bool live = t < a.tokens;
+    uint32_t key[V];
+    float f[V], top = 0.f;
+    double sum = 1.0;
+    load_logits<V>(a, t, sub, f);
+#pragma unroll
+    for (int c = 0; c < V; ++c)
+        f[c] = live && int(expert_of<V>(c, sub)) < a.experts && f[c] > -INFINITY ? fminf(f[c], FLT_MAX) : -INFINITY;
+    if (a.score == SCORE_SOFTMAX) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) key[c] = f[c] > -INFINITY ? order_key(f[c]) : 0;
+        const uint32_t m = largest(key);
+        top = m ? order_value(m) : 0.f;
+        sum = 0.0;
+#pragma unroll
+        for (int c = 0; c < V; ++c) sum += f[c] > -INFINITY ? exp(double(f[c]) - double(top)) : 0.0;
+        sum = row_sum64(sum);
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        key[c] = 0;
+        if (f[c] > -INFINITY) {
+            float k = score_of(a, f[c], top, sum);
+            if (a.bias) k += a.bias[expert_of<V>(c, sub)];
+            if (k > -INFINITY) key[c] = order_key(fminf(k, FLT_MAX));
+        }
+    }
+    if (a.groups > 1) {
+        const uint32_t per = uint32_t(a.experts / a.groups);
+        uint32_t mine = 0;                                 // lane g: group g's key
+        for (int g = 0; g < a.groups; ++g) {
+            uint32_t in[V];
+#pragma unroll
+            for (int c = 0; c < V; ++c) in[c] = expert_of<V>(c, sub) / per == uint32_t(g) ? key[c] : 0;
+            const Choice best = choose<V>(in, a.group_top, sub);
+            const uint32_t one = row_max(sub == 0 ? best.key : 0), two = row_max(sub == 1 ? best.key : 0);
+            const float sum2 = two ? order_value(one) + order_value(two) : order_value(one);
+            if (uint32_t(g) == sub) mine = one ? order_key(fminf(sum2, FLT_MAX)) : 0;
+        }
+        uint32_t keys[1] = {mine};
+        const Choice chosen = choose<1>(keys, a.top_groups, sub);
+        uint32_t mask = chosen.key ? 1u << chosen.id : 0;
+        mask |= row_ror<8>(mask);
+        mask |= row_ror<4>(mask);
+        mask |= row_ror<2>(mask);
+        mask |= row_ror<1>(mask);
+#pragma unroll
+        for (int c = 0; c < V; ++c) key[c] = (mask >> min(expert_of<V>(c, sub) / per, 31u)) & 1u ? key[c] : 0;
+    }
+    const Choice r = choose<V>(key, a.top_k, sub);
+    float w = 0.f;
+    if (r.key) {
+        const int64_t o = t * a.ld + r.id;
+        const float l = a.type == VT_F32 ? static_cast<const float*>(a.logits)[o] : bf16_value(static_cast<const uint16_t*>(a.logits)[o]);
+        w = score_of(a, fminf(l, FLT_MAX), top, sum);
+    }
+    if (a.renorm) {
+        const float all = row_sum(w);
+        w = all > 0.f ? w / all : 0.f;                     // every chosen score may be 0
+    }
+    if (live && int(sub) < a.top_k) {
+        const int64_t o = t * a.top_k + sub;
+        a.ids[o] = int32_t(r.id);
+        a.weights[o] = w * a.scale;
+        if (r.key) atomicAdd(cnt + r.id, 1u);
     }
 }
 
@@ -165,7 +284,7 @@ __device__ void select(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cn
 // bits each, so that 16-byte loads bring eight experts' and all of a thread's
 // loads are on their way at once, from the kernel's first instruction on.
 // V: logits a lane.
-template <int PHASE, int V>
+template <int PHASE, int V, bool SCORED>
 __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     __shared__ uint32_t cnt[PHASE == 1 ? 1 : kRW][kMaxExperts];     // slots of each wave, then the next place of each
     __shared__ uint32_t wave_total[kMaxExperts / 64];
@@ -199,7 +318,9 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     if (PHASE != 2) {
         for (int64_t t = t_lo; t < t_hi; t += 4) {
             const int64_t mine = t + (lane >> 4);
-            select<V>(a, mine < t_hi ? mine : a.tokens, sub, cnt[PHASE == 1 ? 0 : wave]);
+            uint32_t* const counts_of = cnt[PHASE == 1 ? 0 : wave];
+            if (SCORED) select_scored<V>(a, mine < t_hi ? mine : a.tokens, sub, counts_of);
+            else select<V>(a, mine < t_hi ? mine : a.tokens, sub, counts_of);
         }
     } else {
         if (id >= 0) atomicAdd(&cnt[wave][id], 1u);
@@ -341,28 +462,35 @@ void route_blocks(int64_t tokens, int32_t* blocks, int32_t* per_block) {
 }
 
 namespace {
-template <int V>
+template <int V, bool SCORED>
 hipError_t launch(const RouteArgs& a, hipStream_t s) {
     if (a.blocks == 1) {
-        route_kernel<0, V><<<1, kRT, 0, s>>>(a);
+        route_kernel<0, V, SCORED><<<1, kRT, 0, s>>>(a);
         return hipGetLastError();
     }
     // four tokens a wave at a time, as many waves as the block's tokens keep busy
-    route_kernel<1, V><<<unsigned(a.blocks), unsigned(std::min(kRT, a.per_block * 16)), 0, s>>>(a);
+    route_kernel<1, V, SCORED><<<unsigned(a.blocks), unsigned(std::min(kRT, a.per_block * 16)), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    route_kernel<2, 1><<<unsigned(a.blocks), kRT, 0, s>>>(a);
+    route_kernel<2, 1, false><<<unsigned(a.blocks), kRT, 0, s>>>(a);
     return hipGetLastError();
 }
 }  // namespace
 
+namespace {
+template <bool SCORED>
+hipError_t launch_width(const RouteArgs& a, hipStream_t s) {
+    if (a.experts <= 16) return launch<1, SCORED>(a, s);
+    if (a.experts <= 32) return launch<2, SCORED>(a, s);
+    if (a.experts <= 64) return launch<4, SCORED>(a, s);
+    if (a.experts <= 128) return launch<8, SCORED>(a, s);
+    if (a.experts <= 256) return launch<16, SCORED>(a, s);
+    return launch<32, SCORED>(a, s);
+}
+}  // namespace
+
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-    if (a.experts <= 16) return launch<1>(a, s);
-    if (a.experts <= 32) return launch<2>(a, s);
-    if (a.experts <= 64) return launch<4>(a, s);
-    if (a.experts <= 128) return launch<8>(a, s);
-    if (a.experts <= 256) return launch<16>(a, s);
-    return launch<32>(a, s);
+    return a.score == SCORE_LOGIT ? launch_width<false>(a, s) : launch_width<true>(a, s);
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {

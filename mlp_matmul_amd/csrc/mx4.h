@@ -1,0 +1,37 @@
+// Argument blocks and launchers of the microscaled 4-bit operators.
+//
+// The format: the 32 numbers of columns 32b .. 32b+31 of a row share the power
+// of two 2^(s - 127), s an unsigned byte (255: no number), each is one of
+// +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} times it, held in four bits, sign first; the
+// even column's lie in the low half of their byte.
+#pragma once
+
+#include "experts.h"
+
+namespace uwk {
+
+constexpr int kMx4Block = 32;        // numbers that share a scale
+
+struct Mx4Mat {
+    const uint8_t* codes;       // rows of C/2 bytes, ldc apart
+    const uint8_t* scales;      // rows of C/32 bytes, lds apart
+    int64_t ldc, lds;           // multiples of 16
+};
+
+// One matmul (or the gate/up pair) with 4-bit weights over rows grouped by
+// expert.  g.w is not read; the rows of X are bf16 (g.X, g.ldx) or 4-bit (x).
+struct Mx4Args {
+    GroupArgs g;
+    Mx4Mat w[2];                // [1]: up of the pair
+    Mx4Mat x;
+};
+
+hipError_t launch_mx4_quantize(const void* X, int type, int64_t ldx, int64_t rows, int64_t cols, uint8_t* codes,
+                               int64_t ldc, uint8_t* scales, int64_t lds, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4Mat& m, int64_t rows, int64_t cols, void* out, int type, int64_t ldo,
+                                 hipStream_t s);
+
+// The product of any shape (x4: the rows of X are 4-bit too).
+hipError_t launch_mx4(bool x4, bool pair, const Mx4Args& a, hipStream_t s);
+
+}  // namespace uwk
