@@ -20,9 +20,23 @@ __device__ __forceinline__ uint32_t spread_unit(uint32_t total, uint32_t id) {
     return xcd * q + min(xcd, r) + (id >> 3);
 }
 
+// Unit `u` of a group's tiles x bands, as (band, tile): the tiles of a band, or
+// of SIDE bands at a time, one behind the other.
+template <int SIDE>
+__device__ __forceinline__ void band_and_tile(uint32_t u, uint32_t bands, uint32_t tiles, uint32_t& band, uint32_t& tile) {
+    if (SIDE == 1) {
+        band = u / tiles;
+        tile = u % tiles;
+        return;
+    }
+    const uint32_t b0 = u / (SIDE * tiles) * SIDE, in = u - b0 * tiles, n = min(uint32_t(SIDE), bands - b0);
+    band = b0 + in % n;
+    tile = in / n;
+}
+
 // group_tile with offsets, CH * 64 experts at most: expert 64*c + lane of
 // chunk c in this lane.  All loads go out together.
-template <int NT, int CH>
+template <int NT, int CH, int SIDE>
 __device__ __forceinline__ bool group_tile_of(const GroupArgs& a, uint32_t bands, GroupTile& t) {
     const int lane = int(lane_id());
     const int32_t n = int32_t(a.n);
@@ -65,10 +79,10 @@ __device__ __forceinline__ bool group_tile_of(const GroupArgs& a, uint32_t bands
         const uint32_t first = uint32_t(__builtin_amdgcn_readlane(int(lo[c]), l));
         const uint32_t tiles = (nr + NT - 1) / NT;
         const uint32_t before = uint32_t(__builtin_amdgcn_readlane(int(end[c]), l)) - tiles;
-        const uint32_t local = u - before * bands;
+        uint32_t band, i;
+        band_and_tile<SIDE>(u - before * bands, bands, tiles, band, i);
         t.e = 64 * c + l;
-        t.band = int32_t(local / tiles);
-        const uint32_t i = local % tiles;
+        t.band = int32_t(band);
         t.row0 = int64_t(first) + int64_t(i) * NT;
         t.rows = int32_t(min(uint32_t(NT), nr - i * NT));
     }
@@ -80,21 +94,25 @@ __device__ __forceinline__ bool group_tile_of(const GroupArgs& a, uint32_t bands
 // each other (they read the same weights); false past the last one.  The grid
 // holds the most there can be, the host does not know the offsets.  Offsets
 // out of order or out of range are clamped, so no row outside [0, n) is
-// touched.  Every wave finds the unit by itself: no barrier.
-template <int NT>
+// touched.  Every wave finds the unit by itself: no barrier.  SIDE: bands that
+// are walked together, so that units at work at the same time share both
+// operands.
+template <int NT, int SIDE = 1>
 __device__ __forceinline__ bool group_tile(const GroupArgs& a, uint32_t bands, GroupTile& t) {
     if (!a.offsets) {
         const uint32_t tiles = uint32_t((a.n + NT - 1) / NT), total = tiles * bands * uint32_t(a.split);
         if (blockIdx.x >= total) return false;
         const uint32_t u = spread_unit(total, blockIdx.x);
         t.e = 0;
+        uint32_t band, i;
+        band_and_tile<SIDE>(u % (tiles * bands), bands, tiles, band, i);
         t.slice = int32_t(u / (tiles * bands));
-        t.band = int32_t(u / tiles % bands);
-        t.row0 = int64_t(u % tiles) * NT;
+        t.band = int32_t(band);
+        t.row0 = int64_t(i) * NT;
         t.rows = int32_t(min(int64_t(NT), a.n - t.row0));
         return true;
     }
-    return a.E <= 64 ? group_tile_of<NT, 1>(a, bands, t) : group_tile_of<NT, kMaxExperts / 64>(a, bands, t);
+    return a.E <= 64 ? group_tile_of<NT, 1, SIDE>(a, bands, t) : group_tile_of<NT, kMaxExperts / 64, SIDE>(a, bands, t);
 }
 
 // Most units a grid needs: every expert with rows has at most n_e/NT + 1 tiles.

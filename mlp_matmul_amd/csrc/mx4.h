@@ -34,4 +34,12 @@ hipError_t launch_mx4_dequantize(const Mx4Mat& m, int64_t rows, int64_t cols, vo
 // The product of any shape (x4: the rows of X are 4-bit too).
 hipError_t launch_mx4(bool x4, bool pair, const Mx4Args& a, hipStream_t s);
 
+// The kernels behind it.  Up to `rows` (4, 16 or 32; 16 or 32 4-bit ones) rows an expert before its weights are read
+// again.
+hipError_t launch_mx4_skinny(bool x4, bool pair, const Mx4Args& a, int rows, hipStream_t s);
+int mx4_skinny_waves(int rows, const Mx4Args& a);             // of its workgroups
+// Tiles of weight rows x input rows.
+enum Mx4TileShape { MX4_TILE_SMALL, MX4_TILE_MIDDLE, MX4_TILE_LARGE, MX4_TILE_SHAPES };
+hipError_t launch_mx4_tile(bool x4, bool pair, const Mx4Args& a, Mx4TileShape shape, hipStream_t s);
+
 }  // namespace uwk

@@ -7,98 +7,128 @@
 // two significant bits: a product with a bf16 number is exact in fp32, as it is
 // with another 4-bit one.
 #include <algorithm>
+#include <cmath>
 
-#include "grouped_common.h"
-#include "kernels.h"
 #include "mx4.h"
 
 namespace uwk {
 
 namespace {
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
+// The choice goes by estimated times, in us.  The constants are fitted to 701
+// sizes (one matrix of 64 x 256 to 16000 x 14336 with 1 to 4200 rows, the pair
+// and the single product of 2 to 64 experts), each timed on MI355X with every
+// kernel; what the estimates choose there takes 1.02 times the fastest kernel's
+// time in the geometric mean and 1.4 times at worst.
+//
+// Tiles: a step of a round of workgroups with one here and there, with one on
+// each compute unit, with `per_cu` on each; the launch, and what a round needs
+// before its first step and behind its last, in steps.
+struct TileCost {
+    int mt, nt, per_cu;
+    double few, one, full, launch, around;
+};
+constexpr TileCost kTiles[2][MX4_TILE_SHAPES] = {      // bf16 rows, 4-bit rows
+    {{64, 64, 2, 0.35, 0.45, 0.62, 4.6, 5.1}, {128, 64, 2, 0.42, 0.66, 1.05, 5.2, 3.5}, {256, 128, 1, 1.5, 1.5, 1.5, 2.4, 5.1}},
+    {{64, 64, 4, 0.30, 0.50, 1.07, 4.9, 3.1}, {128, 128, 2, 0.56, 0.97, 1.36, 6.3, 3.8}, {256, 256, 1, 1.5, 2.5, 2.75, 9.3, 3.4}}};
+constexpr int kStepCols[2] = {128, 256};
+// The skinny kernel: a wave's step of 128 columns with few waves and with the
+// chip full of them; the launch, and what a workgroup needs around its steps.
+struct SkinnyCost {
+    double few, full, launch, around;
+};
+constexpr int kSkinnyRows[3] = {4, 16, 32};
+constexpr SkinnyCost kSkinny[2][2][3] = {              // 4-bit rows, pair, rows
+    {{{0.060, 1.05, 2.5, 2.7}, {0.17, 0.82, 2.9, 2.4}, {0.20, 0.86, 3.3, 2.5}},
+     {{0.21, 1.27, 3.1, 2.4}, {0.10, 0.81, 3.3, 3.4}, {0.09, 0.68, 3.6, 4.1}}},
+    {{{}, {0.044, 0.92, 3.2, 1.9}, {0.054, 0.84, 3.1, 2.0}}, {{}, {0.15, 1.08, 4.5, 1.4}, {0.05, 0.84, 4.0, 2.6}}}};
+// Bytes a us of the weights, and the share of them that a further tile of rows reads again: tiles of one band run side
+// by side and find part of them in a cache.
+constexpr double kStream = 5e6, kAgain = 0.3;
 
-// A 16 x 16 tile a wave straight from memory, 128 columns a step; four waves
-// share 16 input rows.
-template <bool X4, bool PAIR>
-__global__ __launch_bounds__(256) void mx4_simple_kernel(Mx4Args a, uint32_t bands) {
-    GroupTile t;
-    if (!group_tile<16>(a.g, bands, t)) return;
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t lane = uint32_t(tid) & 63u, q = lane >> 4, rl = lane & 15u;
-    const int64_t R = a.g.R, row0 = int64_t(t.band) * 64 + wave * 16;
-    if (row0 >= R) return;
-    const int64_t wr = int64_t(t.e) * R + min(row0 + rl, R - 1);
-    const int64_t xr = group_x_index(a.g, t.row0 + min(rl, uint32_t(t.rows) - 1u));
-    const uint32_t blocks = uint32_t(a.g.C) / kMx4Block;
-    constexpr int M = PAIR ? 2 : 1;
-    f32x4_t acc[M] = {};
-    for (uint32_t b0 = 0; b0 < blocks; b0 += 4) {
-        const bool in = b0 + q < blocks;                 // a lane behind the last block multiplies zeros
-        const uint32_t b = in ? b0 + q : 0u;
-        i32x8_t xc{};
-        uint32_t xs = 127;
-        u32x4_t xv[4];
-        if (X4) {
-            const u32x4_t c = load16(a.x.codes + xr * a.x.ldc + b * 16u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) xc[k] = in ? int(c[k]) : 0;
-            if (in) xs = a.x.scales[xr * a.x.lds + b];
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                xv[k] = load16(a.g.X + xr * a.g.ldx + b * 32u + uint32_t(k) * 8u);
-                if (!in) xv[k] = u32x4_t{0u, 0u, 0u, 0u};
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            const u32x4_t c = load16(a.w[m].codes + wr * a.w[m].ldc + b * 16u);
-            const uint32_t s = in ? a.w[m].scales[wr * a.w[m].lds + b] : 127u;
-            if (X4) {
-                i32x8_t wc{};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) wc[k] = in ? int(c[k]) : 0;
-                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wc, xc, acc[m], 4, 4, 0, int(s), 0, int(xs));
-            } else {
-                const float scale = __uint_as_float(s << 23);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t d = in ? c[k] : 0u;
-                    const u32x4_t w{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0)),
-                                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1)),
-                                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2)),
-                                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3))};
-                    acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w),
-                                                                     __builtin_bit_cast(bf16x8_t, xv[k]), acc[m], 0, 0, 0);
-                }
-            }
-        }
+struct Problem {
+    bool x4, pair, exact;        // exact: one group, `rows` is no average
+    double groups, rows;
+    const Mx4Args& a;
+
+    // tiles of a group: with rows spread over the groups half a tile is lost on average
+    double tiles(int nt) const { return exact ? double((a.g.n + nt - 1) / nt) : std::max(1.0, rows / nt + 0.5); }
+    double stream_us(double t) const {
+        return groups * double(a.g.R) * double(a.g.C) * (pair ? 2 : 1) * 0.53125 * (1 + kAgain * (t - 1)) / kStream;
     }
-    const uint32_t row = uint32_t(row0) + 4u * q;
-    if (rl >= uint32_t(t.rows) || row >= uint32_t(R)) return;
-    f32x4_t y = acc[0];
-    if (PAIR) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = silu(y[i]) * acc[M - 1][i];
-    }
-    epilogue4(a.g.ep, t.row0 + rl, int(row), a.g.R, y);
+};
+
+double tile_us(const Problem& p, int i) {
+    const TileCost& c = kTiles[p.x4][i];
+    const int mt = p.pair ? c.mt / 2 : c.mt;
+    const double tiles = p.tiles(c.nt), per = p.groups * double((p.a.g.R + mt - 1) / mt) * tiles / p.a.g.cus;
+    const double rounds = double(int64_t(per / c.per_cu)), rest = per - rounds * c.per_cu;
+    double step = rounds * c.full;
+    if (rest > 1) step += c.one + (c.full - c.one) * (rest - 1) / (c.per_cu - 1);
+    else if (rest > 0) step += c.few + (c.one - c.few) * rest;
+    return c.launch + std::max(step * (double(p.a.g.C) / kStepCols[p.x4] + c.around), p.stream_us(tiles) / std::min(1.0, per * 1.5));
 }
 
-template <bool X4, bool PAIR>
-hipError_t launch_simple(const Mx4Args& a, hipStream_t s) {
-    const int64_t bands = (int64_t(a.g.R) + 63) / 64, units = group_units(a.g, 16, bands);
-    if (units > 0x7FFFFFFF) return hipErrorInvalidValue;
-    launch_timed(mx4_simple_kernel<X4, PAIR>, dim3(unsigned(units)), dim3(256), 0, s, a, uint32_t(bands));
-    return hipGetLastError();
+double skinny_us(const Problem& p, int i) {
+    const SkinnyCost& c = kSkinny[p.x4][p.pair][i];
+    const int rows = kSkinnyRows[i], kw = mx4_skinny_waves(rows, p.a), m = p.pair ? 2 : 1;
+    const int x = p.x4 ? std::max(1, rows / 16) : rows / 4, depth = rows == 4 && kw == 8 ? 4 : 2;
+    const int lds = kw * ((m + x) * depth + m + (p.x4 ? x : 0));           // KB
+    const int per_cu = std::max(1, std::min(160 / lds, 32 / kw));
+    const double tiles = p.tiles(rows), rounds = p.groups * double((p.a.g.R + 15) / 16) * tiles / p.a.g.cus / per_cu;
+    const double step = c.few + (c.full - c.few) * std::min(1.0, rounds);
+    return c.launch + std::max(std::max(1.0, rounds) * (std::max(1.0, double(p.a.g.C) / 128 / kw) * step + c.around), p.stream_us(tiles));
+}
+
+struct Choice {
+    bool skinny;
+    int i;
+    double us;
+};
+
+Choice choose(const Problem& p) {
+    Choice best{true, 1, 1e30};
+    auto offer = [&](Choice c) {
+        if (c.us < best.us) best = c;
+    };
+    for (int i = p.x4 ? 1 : 0; i < 3; ++i) offer({true, i, skinny_us(p, i)});
+    for (int i = 0; i < MX4_TILE_SHAPES; ++i) offer({false, i, tile_us(p, i)});
+    return best;
+}
+
+hipError_t run(bool x4, bool pair, const Mx4Args& a, const Choice& c, hipStream_t s) {
+    return c.skinny ? launch_mx4_skinny(x4, pair, a, kSkinnyRows[c.i], s) : launch_mx4_tile(x4, pair, a, Mx4TileShape(c.i), s);
 }
 
 }  // namespace
 
 hipError_t launch_mx4(bool x4, bool pair, const Mx4Args& a, hipStream_t s) {
     if (a.g.n <= 0 || a.g.R <= 0) return hipSuccess;
-    if (x4) return pair ? launch_simple<true, true>(a, s) : launch_simple<true, false>(a, s);
-    return pair ? launch_simple<false, true>(a, s) : launch_simple<false, false>(a, s);
+    const bool exact = !a.g.offsets;
+    const double groups = exact ? 1 : double(std::min<int64_t>(a.g.n, a.g.E));
+    const Choice c = choose({x4, pair, exact, groups, double(a.g.n) / groups, a});
+    if (!exact || c.skinny) return run(x4, pair, a, c, s);
+    // A few rows behind the last whole tile go to the skinny kernel where another
+    // round of tiles would take longer (4097 rows of 14336 x 4096, 4-bit: 159 us
+    // against 164).
+    const int64_t tail = a.g.n % kTiles[x4][c.i].nt;
+    if (tail == 0 || tail > 32 || tail == a.g.n) return run(x4, pair, a, c, s);
+    Mx4Args head = a, rest = a;
+    head.g.n = head.g.x_rows = a.g.n - tail;
+    rest.g.n = rest.g.x_rows = tail;
+    const Choice ch = choose({x4, pair, true, 1, double(head.g.n), head}), cr = choose({x4, pair, true, 1, double(tail), rest});
+    if (ch.us + cr.us >= c.us) return run(x4, pair, a, c, s);
+    if (x4) {
+        rest.x.codes += head.g.n * a.x.ldc;
+        rest.x.scales += head.g.n * a.x.lds;
+    } else {
+        rest.g.X += head.g.n * a.g.ldx;
+    }
+    const int64_t ob = a.g.ep.out_type == VT_BF16 ? 2 : 4, rb = a.g.ep.residual_type == VT_BF16 ? 2 : 4;
+    rest.g.ep.out = static_cast<uint8_t*>(a.g.ep.out) + head.g.n * a.g.ep.ldo * ob;
+    if (a.g.ep.residual) rest.g.ep.residual = static_cast<const uint8_t*>(a.g.ep.residual) + head.g.n * a.g.ep.ldr * rb;
+    const hipError_t e = run(x4, pair, head, ch, s);
+    return e == hipSuccess ? run(x4, pair, rest, cr, s) : e;
 }
 
 }  // namespace uwk
