@@ -74,12 +74,17 @@ __device__ __forceinline__ float order_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// The expert that a lane's value c is: runs of four where V allows a wide load.
+// The expert that a lane's value c is, runs of four where V allows a wide load: part(c) and the lane's own share.
 template <int V>
-__device__ __forceinline__ uint32_t expert_of(int c, uint32_t sub) {
-    constexpr int W = V < 4 ? 1 : 4;
-    return uint32_t(16 * W * (c / W) + c % W) + W * sub;
-}
+struct Experts {
+    static constexpr int W = V < 4 ? 1 : 4;
+    uint32_t lane;
+    __device__ __forceinline__ explicit Experts(uint32_t sub) : lane(W * sub) {}
+    __device__ __forceinline__ uint32_t part(int c) const { return uint32_t(16 * W * (c / W) + c % W); }
+    __device__ __forceinline__ uint32_t operator()(int c) const { return part(c) + lane; }
+};
+template <int V>
+__device__ __forceinline__ uint32_t expert_of(int c, uint32_t sub) { return Experts<V>(sub)(c); }
 
 // The logits of token t (one per DPP row), V a lane.  Every load stays inside
 // the logits and none waits for another.
@@ -128,9 +133,10 @@ struct Choice {
     uint32_t key, id, top;   // lane j's: those of the j-th chosen; the first one's key
 };
 
-// The top_k largest keys, equal ones by the lowest index; taken ones become 0.
-template <int V>
-__device__ __forceinline__ Choice choose(uint32_t (&key)[V], int top_k, uint32_t sub) {
+// The top_k largest keys, equal ones by the lowest index(c); taken ones become 0 (in every lane that holds it, where
+// several hold the same index).
+template <int V, class Index>
+__device__ __forceinline__ Choice choose(uint32_t (&key)[V], int top_k, uint32_t sub, const Index& index) {
     Choice r{0, ~0u, 0};
     for (int j = 0; j < top_k; ++j) {
         const uint32_t m = largest(key), find = max(m, 1u);   // 1 is a NaN's key: with m = 0 nothing is found
@@ -139,8 +145,9 @@ __device__ __forceinline__ Choice choose(uint32_t (&key)[V], int top_k, uint32_t
 #pragma unroll
         for (int c = V - 1; c >= 0; --c) {
             has[c] = key[c] == find;
-            at = has[c] ? expert_of<V>(c, sub) : at;
+            at = has[c] ? index.part(c) : at;              // (the whole index of every value would take V registers)
         }
+        at = at == ~0u ? at : at + index.lane;
         const uint32_t e = row_min(at);
         bool open = m && at == e;                          // this lane has it: its lowest one goes
 #pragma unroll
@@ -175,7 +182,7 @@ __device__ void select(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cn
         for (int c = 0; c < V; ++c) sum += key[c] ? expf(order_value(key[c]) - top) : 0.f;
         sum = row_sum(sum);
     }
-    const Choice r = choose<V>(key, a.top_k, sub);
+    const Choice r = choose<V>(key, a.top_k, sub, Experts<V>(sub));
     const float w = r.key ? expf(order_value(r.key) - order_value(r.top)) : 0.f;
     if (a.renorm) sum = row_sum(w);
     if (live && int(sub) < a.top_k) {
@@ -201,71 +208,170 @@ __device__ __forceinline__ double row_sum64(double v) {
     return v + ror(v, std::integral_constant<int, 1>{});
 }
 
-// The score of a finite logit; top and sum: of the token's softmax.
-__device__ __forceinline__ float score_of(const RouteArgs& a, float l, float top, double sum) {
-    if (a.score == SCORE_SIGMOID) return float(1.0 / (1.0 + exp(-double(l))));
-    return float(exp(double(l) - double(top)) / sum);
+// exp(x) for x <= 708 (0 for those below -708, nearly), to 2^-51: x = n ln 2 + r, the Taylor sum of e^r to the 13th power
+// (|r| <= 0.347, the next term is below 2^-52), times 2^n.
+__device__ __forceinline__ double exp64(double x) {
+    x = fmax(x, -708.0);
+    const double n = rint(x * 1.4426950408889634074);
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.693147180369123816490, x));   // ln 2 in two parts
+    double y = 1.0 / 6227020800.0;
+    y = fma(y, r, 1.0 / 479001600.0);
+    y = fma(y, r, 1.0 / 39916800.0);
+    y = fma(y, r, 1.0 / 3628800.0);
+    y = fma(y, r, 1.0 / 362880.0);
+    y = fma(y, r, 1.0 / 40320.0);
+    y = fma(y, r, 1.0 / 5040.0);
+    y = fma(y, r, 1.0 / 720.0);
+    y = fma(y, r, 1.0 / 120.0);
+    y = fma(y, r, 1.0 / 24.0);
+    y = fma(y, r, 1.0 / 6.0);
+    y = fma(y, r, 0.5);
+    y = fma(y, r, 1.0);
+    y = fma(y, r, 1.0);
+    return ldexp(y, int(n));
+}
+
+// 1 / d for d >= 1, to 2^-52: the hardware's estimate, off by 2^-23, and two steps of Newton's.
+__device__ __forceinline__ double rcp64(double d) {
+    double y = __builtin_amdgcn_rcp(d);
+    y = fma(fma(-d, y, 1.0), y, y);
+    return fma(fma(-d, y, 1.0), y, y);
+}
+
+// Scores, rounded to fp32 once.  Beyond 110 the sigmoid is 0 or 1 there.
+__device__ __forceinline__ float sigmoid_of(float l) {
+    return float(rcp64(1.0 + exp64(-double(fminf(fmaxf(l, -110.f), 110.f)))));
+}
+__device__ __forceinline__ float softmax_of(float l, float top, double scale) { return float(exp64(double(l) - double(top)) * scale); }
+
+// v[c] = f(v[c]) for every c, four at a time in a loop that turns the array round: unrolled, the doubles of all of them
+// would spill (16384 tokens of 256 experts: 43 us).
+template <int V, class F>
+__device__ __forceinline__ void in_fours(float (&v)[V], F&& f) {
+    constexpr int N = V < 4 ? V : 4;
+#pragma unroll 1
+    for (int i = 0; i < V / N; ++i) {
+        float r[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) r[c] = f(v[c]);
+#pragma unroll
+        for (int c = 0; c + N < V; ++c) v[c] = v[c + N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) v[V - N + c] = r[c];
+    }
+}
+
+// The two largest of two pairs (m >= n each).
+__device__ __forceinline__ void merge2(uint32_t& m, uint32_t& n, uint32_t om, uint32_t on) {
+    n = max(min(m, om), max(n, on));
+    m = max(m, om);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false));
+}
+
+// The key of a group with the two largest keys m and n (0: none).
+__device__ __forceinline__ uint32_t group_key(uint32_t m, uint32_t n, int group_top) {
+    if (!m) return 0;
+    const float one = order_value(m);
+    return order_key(fminf(n && group_top > 1 ? one + order_value(n) : one, FLT_MAX));
+}
+
+// Clears the keys outside the top_groups groups with the largest keys.
+template <int V>
+__device__ __forceinline__ void choose_groups(const RouteArgs& a, uint32_t (&key)[V], uint32_t sub) {
+    const uint32_t per = uint32_t(a.experts / a.groups);
+    constexpr int NC = V < 4 ? 1 : V / 4;
+    if (V >= 4 && (per & 3u) == 0 && per <= 64 && (64u % per) == 0) {
+        // a lane's runs of four each lie in one group, of `lanes` neighbouring lanes
+        const uint32_t lanes = per / 4;
+        uint32_t g[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            uint32_t m = max(key[4 * c], key[(4 * c + 1) % V]), n = min(key[4 * c], key[(4 * c + 1) % V]);
+            const uint32_t p = key[(4 * c + 2) % V], q = key[(4 * c + 3) % V];
+            merge2(m, n, max(p, q), min(p, q));
+            if (lanes > 1) merge2(m, n, dpp<0xB1>(m), dpp<0xB1>(n));           // lanes 1 0 3 2
+            if (lanes > 2) merge2(m, n, dpp<0x4E>(m), dpp<0x4E>(n));           // lanes 2 3 0 1
+            if (lanes > 4) merge2(m, n, dpp<0x141>(m), dpp<0x141>(n));         // the other half of eight
+            if (lanes > 8) merge2(m, n, dpp<0x140>(m), dpp<0x140>(n));         // the other half of sixteen
+            g[c] = group_key(m, n, a.group_top);
+        }
+        struct {
+            uint32_t per_chunk, lane;
+            __device__ __forceinline__ uint32_t part(int c) const { return uint32_t(c) * per_chunk; }
+        } const index{16u / lanes, sub / lanes};
+        choose<NC>(g, a.top_groups, sub, index);
+#pragma unroll
+        for (int c = 0; c < V; ++c) key[c] = g[c / 4 % NC] ? 0 : key[c];
+        return;
+    }
+    uint32_t mine = 0;                                     // lane g: group g's key
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+        uint32_t m = 0, n = 0;
+#pragma unroll
+        for (int c = 0; c < V; ++c) merge2(m, n, expert_of<V>(c, sub) - uint32_t(g) * per < per ? key[c] : 0, 0);
+        merge2(m, n, row_ror<8>(m), row_ror<8>(n));
+        merge2(m, n, row_ror<4>(m), row_ror<4>(n));
+        merge2(m, n, row_ror<2>(m), row_ror<2>(n));
+        merge2(m, n, row_ror<1>(m), row_ror<1>(n));
+        if (uint32_t(g) == sub) mine = group_key(m, n, a.group_top);
+    }
+    uint32_t keys[1] = {mine};
+    choose<1>(keys, a.top_groups, sub, Experts<1>(sub));
+    const uint64_t left = __builtin_amdgcn_ballot_w64(keys[0] != 0);           // groups that were not taken, of four tokens
+    const uint32_t out = uint32_t(left >> (lane_id() & 48u));
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+        if (!((out >> g) & 1u)) continue;
+#pragma unroll
+        for (int c = 0; c < V; ++c) key[c] = expert_of<V>(c, sub) - uint32_t(g) * per < per ? 0 : key[c];
+    }
 }
 
 // select by scores: key = score + bias, groups of experts by their best keys,
 // then the best keys of the chosen groups.  The weights are the scores.
 template <int V>
-__device__ void select_scored(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt) {
+__device__ void select_scored(const RouteArgs& a, int64_t t, uint32_t sub, uint32_t* cnt, const float* bias) {
     const bool live = t < a.tokens;
     uint32_t key[V];
     float f[V], top = 0.f;
-    double sum = 1.0;
+    double scale = 1.0;
     load_logits<V>(a, t, sub, f);
 #pragma unroll
     for (int c = 0; c < V; ++c)
         f[c] = live && int(expert_of<V>(c, sub)) < a.experts && f[c] > -INFINITY ? fminf(f[c], FLT_MAX) : -INFINITY;
+    // scores in the logits' place, -inf where there is none
     if (a.score == SCORE_SOFTMAX) {
+        float m = f[0];
 #pragma unroll
-        for (int c = 0; c < V; ++c) key[c] = f[c] > -INFINITY ? order_key(f[c]) : 0;
-        const uint32_t m = largest(key);
-        top = m ? order_value(m) : 0.f;
-        sum = 0.0;
-#pragma unroll
-        for (int c = 0; c < V; ++c) sum += f[c] > -INFINITY ? exp(double(f[c]) - double(top)) : 0.0;
-        sum = row_sum64(sum);
+        for (int c = 1; c < V; ++c) m = fmaxf(m, f[c]);
+        const uint32_t k = row_max(m > -INFINITY ? order_key(m) : 0);
+        top = k ? order_value(k) : 0.f;
+        double sum = 0.0;
+        in_fours<V>(f, [&](float l) {
+            sum += l > -INFINITY ? exp64(double(l) - double(top)) : 0.0;
+            return l;
+        });
+        scale = 1.0 / row_sum64(sum);
+        in_fours<V>(f, [&](float l) { return l > -INFINITY ? softmax_of(l, top, scale) : l; });
+    } else {
+        in_fours<V>(f, [&](float l) { return l > -INFINITY ? sigmoid_of(l) : l; });
     }
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-        key[c] = 0;
-        if (f[c] > -INFINITY) {
-            float k = score_of(a, f[c], top, sum);
-            if (a.bias) k += a.bias[expert_of<V>(c, sub)];
-            if (k > -INFINITY) key[c] = order_key(fminf(k, FLT_MAX));
-        }
+        const float k = f[c] + bias[expert_of<V>(c, sub)]; // behind the last expert: -inf, or no number
+        key[c] = k > -INFINITY ? order_key(fminf(k, FLT_MAX)) : 0;
     }
-    if (a.groups > 1) {
-        const uint32_t per = uint32_t(a.experts / a.groups);
-        uint32_t mine = 0;                                 // lane g: group g's key
-        for (int g = 0; g < a.groups; ++g) {
-            uint32_t in[V];
-#pragma unroll
-            for (int c = 0; c < V; ++c) in[c] = expert_of<V>(c, sub) / per == uint32_t(g) ? key[c] : 0;
-            const Choice best = choose<V>(in, a.group_top, sub);
-            const uint32_t one = row_max(sub == 0 ? best.key : 0), two = row_max(sub == 1 ? best.key : 0);
-            const float sum2 = two ? order_value(one) + order_value(two) : order_value(one);
-            if (uint32_t(g) == sub) mine = one ? order_key(fminf(sum2, FLT_MAX)) : 0;
-        }
-        uint32_t keys[1] = {mine};
-        const Choice chosen = choose<1>(keys, a.top_groups, sub);
-        uint32_t mask = chosen.key ? 1u << chosen.id : 0;
-        mask |= row_ror<8>(mask);
-        mask |= row_ror<4>(mask);
-        mask |= row_ror<2>(mask);
-        mask |= row_ror<1>(mask);
-#pragma unroll
-        for (int c = 0; c < V; ++c) key[c] = (mask >> min(expert_of<V>(c, sub) / per, 31u)) & 1u ? key[c] : 0;
-    }
-    const Choice r = choose<V>(key, a.top_k, sub);
+    if (a.groups > 1) choose_groups<V>(a, key, sub);
+    const Choice r = choose<V>(key, a.top_k, sub, Experts<V>(sub));
     float w = 0.f;
     if (r.key) {
         const int64_t o = t * a.ld + r.id;
         const float l = a.type == VT_F32 ? static_cast<const float*>(a.logits)[o] : bf16_value(static_cast<const uint16_t*>(a.logits)[o]);
-        w = score_of(a, fminf(l, FLT_MAX), top, sum);
+        w = a.score == SCORE_SIGMOID ? sigmoid_of(l) : softmax_of(fminf(l, FLT_MAX), top, scale);
     }
     if (a.renorm) {
         const float all = row_sum(w);
@@ -314,12 +420,16 @@ __global__ __launch_bounds__(kRT) void route_kernel(RouteArgs a) {
     } else {
         for (int e = int(lane); e < E; e += 64) cnt[wave][e] = 0;
     }
+    __shared__ __align__(16) float bias[SCORED ? kMaxExperts : 1];
+    if (SCORED) {
+        for (int e = tid; e < E; e += int(blockDim.x)) bias[e] = a.bias ? a.bias[e] : 0.f;
+    }
     __syncthreads();
     if (PHASE != 2) {
         for (int64_t t = t_lo; t < t_hi; t += 4) {
             const int64_t mine = t + (lane >> 4);
             uint32_t* const counts_of = cnt[PHASE == 1 ? 0 : wave];
-            if (SCORED) select_scored<V>(a, mine < t_hi ? mine : a.tokens, sub, counts_of);
+            if constexpr (SCORED) select_scored<V>(a, mine < t_hi ? mine : a.tokens, sub, counts_of, bias);
             else select<V>(a, mine < t_hi ? mine : a.tokens, sub, counts_of);
         }
     } else {
