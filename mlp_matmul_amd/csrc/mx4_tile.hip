@@ -1,5 +1,31 @@
 // Many rows per expert (or a large batch) against 4-bit weights: the matrix
 // units bound the product.
+//
+// A workgroup multiplies MT weight rows (of the pair: MT/2 of each matrix) with NT
+// input rows in steps of 128 columns (bf16 rows) or 256 (4-bit rows): 64 or 128
+// bytes of a weight row, 256 or 128 of an input row.
+//   bf16 rows: the codes become bf16 with their block's scale in one instruction
+//   for two of them, exactly, and go to the 16x16x32 bf16 MFMA; a lane's half block
+//   of codes is its 16 columns of two of those.
+//   4-bit rows: codes and scales go to the scaled 16x16x128 MFMA as they are, a
+//   block a lane; the instruction takes the scale's byte for the half of the step.
+// Sums in fp32.  LDS is filled from memory directly, S buffers deep, chunks of 16
+// bytes exchanged within a row so that the fragments' reads meet no bank twice;
+// a load to LDS costs by the 128-byte lines that it touches (17.5 cycles a KB for
+// whole lines, 32 for half ones, 88 for 16 bytes a row), so the scales come for 512
+// columns at a time, 16 bytes of a row.  Eight bands of weight rows are walked
+// together, so that the workgroups of an XCD share both operands (3-10 %).
+//
+// Measured on MI355X, 8192 x 8192 weights and as many rows, us by tile:
+//   bf16 rows:   64x64 1291,  128x64 1073,  256x128 861 (1.28 PFLOP/s)
+//   4-bit rows:  64x64 533,   128x128 357,  256x256 288 (3.8 PFLOP/s)
+// Small ones for few rows: 777 rows of 14336 x 4096 in bf16 take 128, 106 and 108;
+// 32 experts with 19 rows each on 1024 x 2048 pairs 47, 40 and 62.
+// Of the 256x256 tile's 726 thousand cycles the matrix units work 262, the LDS 213
+// on fragments and 65 on what arrives, and its loads take 143 to issue: two
+// waves a SIMD between barriers hide only part of these behind each other (without
+// loads 428; four waves with tiles of 128x128 take half as long again, and reading a
+// step or more ahead into L2 changes nothing).
 #include <type_traits>
 
 #include "kernels.h"
@@ -29,11 +55,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
     constexpr int SL = SR / 64;                          // those loads
     constexpr int SD = (SL + NW - 1) / NW;
     constexpr int U = S == 2 ? 2 : 3 * SS;               // steps after which all buffers come round
-    constexpr int kLoads = WD + XD;
+    constexpr int XG = XD / G;                           // loads of the rows of one of the G parts of X
+    constexpr int kLoads = WD + XD, kMain = WD + XG;
     constexpr int kRows = PAIR ? MT / 2 : MT;            // rows of a matrix in a tile
-    static_assert(WD * NW * 64 == MT * WC && XD * NW * 64 == NT * XC && SL * 64 == SR && (S == 2 || S == 3), "whole loads");
-    constexpr int kX = MT * WB, kBuf = kX + NT * XB;
+    static_assert(WD * NW * 64 == MT * WC && XG * G * NW * 64 == NT * XC && SL * 64 == SR && (S == 2 || S == 3), "whole loads");
+    static_assert(G == 1 || (G == 2 && S == 2), "the loads that a step waits for");
+    constexpr int kX = MT * WB, kPart = NT / G * XB, kBuf = kX + kPart;
     __shared__ __align__(16) uint8_t buf0[kBuf], buf1[kBuf], buf2[S > 2 ? kBuf : 16];
+    __shared__ __align__(16) uint8_t rest0[G > 1 ? kPart : 16], rest1[G > 1 ? kPart : 16];   // X's second part
     // Two buffers of scales in one array where the waits drain all loads to LDS anyway (behind them room for loads that
     // nobody reads), else three of their own: a read waits for the loads to its array.
     constexpr int kScales = SR * 16;
@@ -60,7 +89,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
     for (int m = 0; m < (PAIR ? 2 : 1); ++m) wb[m] = a.w[m].codes + first * a.w[m].ldc;
     auto matrix = [&](int j) { return PAIR ? (wave * WD + j) * (64 / WC) / kRows : 0; };    // uniform
     auto w_chunk = [&](int j) { return (lane % WC) ^ swizzle<WB>(uint32_t(wave * WD + j) * (64 / WC) + lane / WC); };
-    auto x_chunk = [&](int j) { return (lane % XC) ^ swizzle<XB>(uint32_t(wave * XD + j) * (64 / XC) + lane / XC); };
+    auto x_row = [&](int j) { return uint32_t(wave * XG + j % XG) * (64 / XC) + lane / XC; };   // in its part
+    auto x_chunk = [&](int j) { return (lane % XC) ^ swizzle<XB>(x_row(j)); };
 #pragma unroll
     for (int j = 0; j < WD; ++j) {
         const uint32_t r = uint32_t(wave * WD + j) * (64 / WC) + lane / WC;
@@ -68,7 +98,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
     }
 #pragma unroll
     for (int j = 0; j < XD; ++j) {
-        const uint32_t r = uint32_t(wave * XD + j) * (64 / XC) + lane / XC;
+        const uint32_t r = uint32_t(j / XG) * (NT / G) + x_row(j);
         const int64_t x = group_x_index(a.g, t.row0 + min(r, uint32_t(t.rows) - 1u));
         xp[j] = (X4 ? a.x.codes + x * a.x.ldc : reinterpret_cast<const uint8_t*>(a.g.X + x * a.g.ldx)) + x_chunk(j) * 16u;
     }
@@ -103,14 +133,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
             }
         }
     };
+    auto rest = [&](int i) -> uint8_t* { return i == 0 ? rest0 : rest1; };
     // steps past the end load the last one again: the waits count the same loads in every step
-    auto load = [&](uint32_t s, int i) {
+    // loads j0 .. j1 - 1: W's, those of X's first part, of its second
+    auto load = [&](uint32_t s, int i, int j0, int j1) {
         uint8_t* const b = buffer(i);
         s = min(s, steps - 1u);
 #pragma unroll
-        for (int j = 0; j < WD; ++j) dma16(wb[matrix(j)] + uint64_t(s) * WB + woff[j], b + (wave * WD + j) * 1024);
-#pragma unroll
-        for (int j = 0; j < XD; ++j) dma16(xp[j] + uint64_t(s) * XB, b + kX + (wave * XD + j) * 1024);
+        for (int j = j0; j < j1; ++j) {
+            if (j < WD) dma16(wb[matrix(j)] + uint64_t(s) * WB + woff[j < WD ? j : 0], b + (wave * WD + j) * 1024);
+            else dma16(xp[j < WD ? 0 : j - WD] + uint64_t(s) * XB, (j < kMain ? b + kX : rest(i)) + (wave * XG + (j - WD) % XG) * 1024);
+        }
     };
 
     // fragments of half h of a step: 4-bit rows' 8 blocks, lane q's block 2q + h; bf16 rows' half h of each of 4 blocks,
@@ -136,7 +169,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
         ia[h] = (uint32_t(a_block(0)) * 16u + rl) * WB + ((X4 ? 2u * q + uint32_t(h) : q) ^ swizzle<WB>(rl)) * 16u;
 #pragma unroll
         for (int k = 0; k < BK; ++k)
-            ib[h][k] = kX + (uint32_t(wn * FN) * 16u + rl) * XB + ((X4 ? 2u * q + uint32_t(h) : 4u * q + uint32_t(2 * h + k)) ^ swizzle<XB>(rl)) * 16u;
+            ib[h][k] = (uint32_t(wn * FG) * 16u + rl) * XB + ((X4 ? 2u * q + uint32_t(h) : 4u * q + uint32_t(2 * h + k)) ^ swizzle<XB>(rl)) * 16u;
     }
     auto read_a = [&](const uint8_t* b, int h, FragsA& f) {
         const uint8_t* const p = b + ia[h];
@@ -147,12 +180,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
             else f.a[i] = *reinterpret_cast<const u32x2_t*>(p + (o + 8 * h));
         }
     };
-    auto read_b = [&](const uint8_t* b, int h, int g, FragsB& f) {
+    auto read_b = [&](const uint8_t* b, int h, FragsB& f) {
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
             const uint8_t* const p = b + ib[h][k];
 #pragma unroll
-            for (int i = 0; i < FG; ++i) f.B[i][k] = *reinterpret_cast<const u32x4_t*>(p + (g * FG + i) * 16 * XB);
+            for (int i = 0; i < FG; ++i) f.B[i][k] = *reinterpret_cast<const u32x4_t*>(p + i * 16 * XB);
         }
     };
     // of step s
@@ -160,7 +193,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
     auto read_scales = [&](uint32_t s, int i, Scales& f) {
         // indexes that the compiler can't take apart, as those of the fragments
         const uint32_t o = so + (S == 2 ? (s / SS & 1u) * kScales + s % SS * KB : uint32_t(i % SS * KB));
-        uint32_t a0 = o + uint32_t(wm * (PAIR ? FM / 2 : FM)) * 256u, b0 = o + uint32_t(MT / 16 + wn * FN) * 256u;
+        uint32_t a0 = o + uint32_t(wm * (PAIR ? FM / 2 : FM)) * 256u, b0 = o + uint32_t(MT / 16 + wn * FG) * 256u;
         asm("" : "+v"(a0));
         if (X4) asm("" : "+v"(b0));
         const uint8_t* const b = scales_of(i);
@@ -170,14 +203,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
             f.a[k] = X4 ? *reinterpret_cast<const uint16_t*>(p) : *p;
         }
 #pragma unroll
-        for (int k = 0; k < (X4 ? FN : 0); ++k) f.b[k] = *reinterpret_cast<const uint16_t*>(b + b0 + k * 256);
+        for (int k = 0; k < (X4 ? FN : 0); ++k) f.b[k] = *reinterpret_cast<const uint16_t*>(b + b0 + (k / FG * (NT / 16 / G) + k % FG) * 256);
     };
     f32x4_t acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    auto mma = [&](auto h, int g, const FragsA& fa, const FragsB& fb, const Scales& sc) {
+    auto mma = [&](auto h, int g, const FragsA& fa, const FragsB& fb, const Scales& sc, auto behind) {
         constexpr int H = decltype(h)::value;
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -194,35 +227,45 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
                         acc[i][g * FG + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8_t, fb.B[j][k]), acc[i][g * FG + j], 0, 0, 0);
                 }
             }
+            behind(i);
         }
     };
     using H0 = std::integral_constant<int, 0>;
     using H1 = std::integral_constant<int, 1>;
 
-    // Step s, i modulo U, in P phases of one half of the columns and one G-th of the
-    // input rows: each reads the next one's fragments.  Before the last one the
-    // barrier, and the loads S steps ahead.  The scales of a step are read in the
-    // one before it, so that their buffer is free in the last of its steps.
+    // Step s, i modulo U, in P phases of one part of the input rows and one half of
+    // the columns: each reads the next one's fragments.  After the first one a
+    // step's buffer is free but for X's second part, which is free before the last
+    // one; then come the barriers and the loads S steps ahead.  The scales of a step
+    // are read in the one before it, so that their buffer is free in the last of
+    // its steps.
     FragsA fa[2];
     FragsB fb[2];
     Scales sc;
-    auto read_phase = [&](const uint8_t* b, int p) {
-        if (p % G == 0) read_a(b, p / G, fa[p / G]);
-        read_b(b, p / G, p % G, fb[p % 2]);
+    auto read_phase = [&](int i, int p) {
+        if (p < 2) read_a(buffer(i), p, fa[p]);
+        read_b(p < 2 ? buffer(i) + kX : rest(i), p % 2, fb[p % 2]);
     };
-    auto mma_phase = [&](int p) {
-        if (p / G) mma(H1{}, p % G, fa[1], fb[p % 2], sc);
-        else mma(H0{}, p % G, fa[0], fb[p % 2], sc);
+    auto mma_phase = [&](int p, auto behind) {
+        if (p % 2) mma(H1{}, p / 2, fa[1], fb[1], sc, behind);
+        else mma(H0{}, p / 2, fa[0], fb[0], sc, behind);
     };
     auto step = [&](uint32_t s, int i) {
 #pragma unroll
         for (int p = 0; p + 1 < P; ++p) {
-            read_phase(buffer(i % S), p + 1);
-            mma_phase(p);
+            read_phase(i % S, p + 1);
+            mma_phase(p, [](int) {});
             __builtin_amdgcn_sched_barrier(0);
+            if (G > 1 && p == 0) {
+                wait_vm<63, true>();                     // this wave's fragments are here
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                load(s + S, i % S, 0, kMain);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         // the next step's loads and this step's fragments are here
-        wait_vm<(S - 2) * kLoads, true>();
+        wait_vm<(G > 1 ? kMain : (S - 2) * kLoads), true>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         Scales next;
@@ -230,10 +273,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
         __builtin_amdgcn_sched_barrier(0);
         if (S == 2) load_scales(s / SS + 2, 0, s % SS == SS - 1);
         else if (i % SS == SS - 1) load_scales(s / SS + 3, i, true);   // before the columns': the waits count those alone
-        load(s + S, i % S);
+        if (G > 1) load(s + S, i % S, kMain, kLoads);
         __builtin_amdgcn_sched_barrier(0);
-        read_phase(buffer((i + 1) % S), 0);
-        mma_phase(P - 1);
+        read_phase((i + 1) % S, 0);
+        if (G > 1) {
+            mma_phase(P - 1, [](int) {});
+        } else {
+            // the loads among the products (2 % faster than before them; with two parts 2 % slower)
+            __builtin_amdgcn_sched_barrier(0);
+            mma_phase(P - 1, [&](int k) {
+                __builtin_amdgcn_sched_barrier(0);
+                load(s + S, i % S, kLoads * k / FM, kLoads * (k + 1) / FM);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        }
         sc = next;
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -244,14 +297,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            load(uint32_t(i), i);
+            load(uint32_t(i), i, 0, kLoads);
             __builtin_amdgcn_sched_barrier(0);           // in this order: the waits count them
         }
-        wait_vm<(S - 1) * (WD + XD), true>();
+        wait_vm<(S - 1) * kLoads, true>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         read_scales(0, 0, sc);
-        read_phase(buf0, 0);
+        read_phase(0, 0);
         uint32_t s = 0;
         for (; s + U <= steps; s += U) {
 #pragma unroll
@@ -274,7 +327,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
 #pragma unroll
         for (int j = 0; j < XD; ++j) {
             const uint32_t c = x_chunk(j) < left * (XC / KB) ? 0u : x_chunk(j) * 16u;
-            dma16(xp[j] + uint64_t(steps) * XB - c, buf0 + kX + (wave * XD + j) * 1024);
+            dma16(xp[j] + uint64_t(steps) * XB - c, (j < XG ? buf0 + kX : rest0) + (wave * XG + j % XG) * 1024);
         }
         load_scales(steps / SS, 0, true);
         __builtin_amdgcn_s_waitcnt(0);
@@ -282,8 +335,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
         read_scales(steps, int(steps % SS), sc);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            read_phase(buf0, p);
-            const int h = p / G;
+            read_phase(0, p);
+            const int h = p % 2;
             if ((X4 ? 2u * q + uint32_t(h) : q) >= left) {
                 FragsA& f = fa[h];
 #pragma unroll
@@ -299,7 +352,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
 #pragma unroll
                     for (int k = 0; k < BK; ++k) fb[p % 2].B[i][k] = u32x4_t{0u, 0u, 0u, 0u};
             }
-            mma_phase(p);
+            mma_phase(p, [](int) {});
         }
         __syncthreads();
     }
@@ -311,7 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
     constexpr int OM = PAIR ? FM / 2 : FM;
     float* const part = reinterpret_cast<float*>(buf0);
     PartEpilogue<kRows, 16 * WN, 64 * NW, ES> out(a.g.ep, part, t, row0, a.g.R, tid);
-    auto rows_of = [](int p) { return [p](int n) { return ((n / 16) * FN + p) * 16 + n % 16; }; };
+    auto rows_of = [](int p) { return [p](int n) { return p / FG * (NT / G) + ((n / 16) * FG + p % FG) * 16 + n % 16; }; };
     out.load(rows_of(0));
 #pragma unroll 1
     for (int p = 0; p < FN; ++p) {
