@@ -536,7 +536,7 @@ int64_t uw_moe_scratch_bytes(int compressed, int64_t tokens, int experts, int to
  * Equal keys, of groups and of experts, go by the lowest index.
  *   ids[t][j]     the expert of the j-th largest key
  *   weights[t][j] scale * s, or scale * s / (the sum of the chosen s) with
- *                 renormalize; 0 where that sum is 0
+ *                 renormalize; 0 where that sum is 0.  scale is finite
  * offsets, order, place, the logits' types and strides, -inf and NaN logits, tokens
  * with fewer experts than top_k, limits, scratch and its size as in
  * uw_moe_route; an expert whose bias is -inf or NaN is never chosen.  groups

@@ -415,6 +415,8 @@ def _value_type(t, name):
 
 def _matrix_arg(t, name, rows=None, cols=None):
     """Row stride of a 2-D tensor whose rows are contiguous."""
+    if isinstance(t, Mx4Matrix):
+        raise ValueError(f"{name} cannot be an Mx4Matrix here")
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}], "
                          f"not {list(t.shape)}")
@@ -424,6 +426,8 @@ def _matrix_arg(t, name, rows=None, cols=None):
 
 
 def _x_arg(X, cols=None):
+    if isinstance(X, Mx4Matrix):
+        raise ValueError("X must be bfloat16: only products with Mx4Matrix weights, but moe_experts, take it as an Mx4Matrix")
     if X.dtype != _torch().bfloat16:
         raise ValueError(f"X must be bfloat16, not {X.dtype}")
     ld = _matrix_arg(X, "X", None, cols)
@@ -457,7 +461,7 @@ def _index_arg(t, name, shape):
 def _weight_arg(W, experts, name="W"):
     """(bf16 pointer, descriptor, rows, cols) of one expert's matrix."""
     if isinstance(W, Mx4Matrix):
-        raise ValueError(f"{name} is an Mx4Matrix: the other weights must be too")
+        raise ValueError(f"{name} is an Mx4Matrix and the other weights are not")
     if isinstance(W, DeviceMatrix):
         n = experts or 1
         if W.rows % n:
@@ -788,6 +792,8 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     if ctx is not None:
         with ctx:
             return moe_layer(gate, up, down, X, logits, top_k, renormalize, residual, out, out_dtype, scratch)
+    if any(isinstance(m, Mx4Matrix) for m in (gate, up, down)):
+        raise ValueError("moe_layer takes no Mx4Matrix: moe_route and moe_experts do its work with them")
     tokens, experts = X.shape[0], logits.shape[-1]
     ldl, kind = _matrix_arg(logits, "logits", tokens), _value_type(logits, "logits")
     gw, gd, F, H = _weight_arg(gate, experts, "gate")
@@ -900,6 +906,8 @@ def mx4_dequantize(M: Mx4Matrix, out=None, out_dtype=None, stream=None):
     if ctx is not None:
         with ctx:
             return mx4_dequantize(M, out, out_dtype)
+    if not isinstance(M, Mx4Matrix):
+        raise ValueError("M must be an Mx4Matrix")
     out, ldo, kind = _out_arg(out, M.rows, M.cols, out_dtype, dev)
     check(lib().uw_mx4_dequantize(ct.byref(M.mx4), out.data_ptr(), kind, ldo, _current_stream(dev)), "uw_mx4_dequantize")
     return out

@@ -1,6 +1,8 @@
 // C ABI entry points of the epilogue matmul and of the mixture-of-experts
 // operators: argument checks, scratch layout and composition.  See unweight.h
 // for the contract.
+#include <cmath>
+
 #include "capi_experts.h"
 
 using namespace uw;
@@ -145,6 +147,7 @@ int uw_moe_route_scored(const void* logits, int logits_type, int64_t ld, int64_t
         if (top_groups < 1 || top_groups > groups) return bad(who, "top_groups must be 1..groups");
         if (group_top < 1 || group_top > 2) return bad(who, "group_top must be 1 or 2");
         if (int64_t(top_groups) * (experts / groups) < top_k) return bad(who, "the chosen groups have fewer than top_k experts");
+        if (!std::isfinite(scale)) return bad(who, "scale must be finite");
         if (!aligned16(bias)) return bad(who, "misaligned bias");
         const uwk::RouteArgs a{logits, ld,  tokens,  logits_type, experts, top_k, renormalize != 0, ids, weights,
                                offsets, order, place, nullptr, 0, 0, score, bias, groups, top_groups, group_top, scale};

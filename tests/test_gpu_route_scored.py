@@ -11,6 +11,7 @@ import pytest
 
 import mlp_matmul_amd as uw
 from tests.gpu_util import print_case
+from tests.mx4_cases import ROUTES
 from tests.mx4_util import route_ref
 from tests.test_gpu_experts import activate, f64, make_weight, torch_cuda  # noqa: F401
 from tests.test_gpu_mx4 import weight
@@ -40,10 +41,7 @@ def logits_of(torch, seed, tokens, experts, pad=0, bf16=False):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
-@pytest.mark.parametrize("tokens,experts,top_k,groups,top_groups", [
-    (1, 1, 1, 1, 1), (1, 8, 2, 1, 1), (3, 16, 4, 4, 2), (64, 64, 6, 8, 3), (65, 60, 5, 12, 5), (17, 40, 3, 2, 1),
-    (200, 256, 8, 8, 4), (130, 160, 6, 16, 3), (33, 512, 16, 16, 16), (500, 96, 8, 3, 2), (70, 7, 2, 7, 3),
-    (2000, 128, 8, 1, 1), (129, 14, 1, 14, 1)])
+@pytest.mark.parametrize("tokens,experts,top_k,groups,top_groups", ROUTES)
 def test_routing(torch_cuda, tokens, experts, top_k, groups, top_groups, score):
     torch = torch_cuda
     for i, (biased, group_top, renorm, scale) in enumerate(((True, 2, True, 2.5), (False, 1, False, 1.0), (True, 1, True, 1.0))):
