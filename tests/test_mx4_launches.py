@@ -73,3 +73,22 @@ def test_the_experts_are_three_products_and_a_sum(recorder):  # noqa: F811
         at(10), at(11), None, 0, 0, at(13), 1, 96, at(14), 1 << 24, None)))]
     assert rcs == [0] and len(names) == 3, (rcs, names)
     assert names[0].startswith("mx4_") and names[1].startswith("mx4_") and names[2].startswith("combine_kernel"), names
+
+
+def test_more_numbers_than_a_launch_takes(recorder):  # noqa: F811
+    """2^32 - 1 eights of numbers a launch: the rest of the rows follow, where the first ones end."""
+    L, rows, cols = recorder.lib, (1 << 21) + 5, 1 << 15
+    rcs = []
+    seen = recorder.launches(lambda: rcs.append(L.uw_mx4_quantize(1 << 40, 1, cols, rows, cols, 1 << 50, cols // 2, 1 << 55,
+                                                                  cols // 32, None)), 72)
+    assert rcs == [0] and [k for k, *_ in seen] == ["mx4_quantize_kernel<false>"] * 3
+    at, left = 0, rows
+    for _, grid, block, raw in seen:
+        X, _, codes, scales, ld, ldc, lds = (int.from_bytes(raw[8 * i:8 * i + 8], "little") for i in range(7))
+        eights, total = (int.from_bytes(raw[56 + 4 * i:60 + 4 * i], "little") for i in range(2))
+        n = total // eights
+        assert total == n * eights and eights == cols // 8 and grid[0] * block[0] * 4 >= total
+        assert (X, codes, scales) == ((1 << 40) + at * cols * 2, (1 << 50) + at * cols // 2, (1 << 55) + at * cols // 32)
+        assert (ld, ldc, lds) == (cols, cols // 2, cols // 32)
+        at, left = at + n, left - n
+    assert left == 0
