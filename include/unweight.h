@@ -558,7 +558,9 @@ int uw_moe_route_scored(const void* logits, int logits_type, int64_t ld, int64_t
  * their range) and are added in fp32.
  *   codes   [rows, cols/2] bytes, the even column in the low half
  *   scales  [rows, cols/32] bytes
- * cols is a multiple of 32; rows lie ldc and lds bytes apart, multiples of 16.
+ * cols is a multiple of 32; rows lie ldc and lds bytes apart, multiples of 16
+ * (long rows of codes at multiples of 128, their cache lines, are multiplied
+ * faster).
  * Kernels may read, and ignore, the bytes of the 16-byte unit in which a row of
  * scales ends.  Rows of one expert's matrix span less than 2^31 bytes. */
 typedef struct {

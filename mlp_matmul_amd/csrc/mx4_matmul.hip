@@ -15,22 +15,27 @@ namespace uwk {
 
 namespace {
 
-// The choice goes by estimated times, in us.  The constants are fitted to 701
-// sizes (one matrix of 64 x 256 to 16000 x 14336 with 1 to 4200 rows, the pair
+// The choice goes by estimated times, in us.  The constants are fitted to 1121
+// sizes (one matrix of 64 x 256 to 16000 x 14336 with 1 to 9000 rows, the pair
 // and the single product of 2 to 64 experts), each timed on MI355X with every
-// kernel; what the estimates choose there takes 1.02 times the fastest kernel's
-// time in the geometric mean and 1.4 times at worst.
+// kernel; what the estimates choose there takes 1.01 times the fastest kernel's
+// time in the geometric mean and 1.34 times at worst.
 //
 // Tiles: a step of a round of workgroups with one here and there, with one on
 // each compute unit, with `per_cu` on each; the launch, and what a round needs
-// before its first step and behind its last, in steps.
+// before its first step and behind its last, in steps, and for columns behind the
+// last whole step.
 struct TileCost {
     int mt, nt, per_cu;
-    double few, one, full, launch, around;
+    double few, one, full, launch, around, tail;
 };
 constexpr TileCost kTiles[2][MX4_TILE_SHAPES] = {      // bf16 rows, 4-bit rows
-    {{64, 64, 2, 0.35, 0.45, 0.62, 4.6, 5.1}, {128, 64, 2, 0.42, 0.66, 1.05, 5.2, 3.5}, {256, 128, 1, 1.5, 1.5, 1.5, 2.4, 5.1}},
-    {{64, 64, 4, 0.30, 0.50, 1.07, 4.9, 3.1}, {128, 128, 2, 0.56, 0.97, 1.36, 6.3, 3.8}, {256, 256, 1, 1.5, 2.5, 2.75, 9.3, 3.4}}};
+    {{64, 64, 2, 0.27, 0.48, 0.60, 4.8, 6.1, 2.5},
+     {128, 64, 2, 0.35, 0.70, 0.99, 5.7, 4.1, 2.0},
+     {256, 128, 1, 1.34, 1.62, 1.52, 5.6, 5.5, 1.5}},
+    {{64, 64, 4, 0.30, 0.55, 1.01, 5.0, 3.3, 1.1},
+     {128, 128, 2, 0.69, 1.08, 1.24, 5.4, 4.9, 0.8},
+     {256, 256, 1, 1.25, 1.72, 1.68, 7.8, 8.0, 5.9}}};
 constexpr int kStepCols[2] = {128, 256};
 // The skinny kernel: a wave's step of 128 columns with few waves and with the
 // chip full of them; the launch, and what a workgroup needs around its steps.
@@ -66,7 +71,8 @@ double tile_us(const Problem& p, int i) {
     double step = rounds * c.full;
     if (rest > 1) step += c.one + (c.full - c.one) * (rest - 1) / (c.per_cu - 1);
     else if (rest > 0) step += c.few + (c.one - c.few) * rest;
-    return c.launch + std::max(step * (double(p.a.g.C) / kStepCols[p.x4] + c.around), p.stream_us(tiles) / std::min(1.0, per * 1.5));
+    const double around = c.around + (p.a.g.C % kStepCols[p.x4] ? c.tail : 0);
+    return c.launch + std::max(step * (double(p.a.g.C) / kStepCols[p.x4] + around), p.stream_us(tiles) / std::min(1.0, per * 1.5));
 }
 
 double skinny_us(const Problem& p, int i) {
@@ -109,8 +115,8 @@ hipError_t launch_mx4(bool x4, bool pair, const Mx4Args& a, hipStream_t s) {
     const Choice c = choose({x4, pair, exact, groups, double(a.g.n) / groups, a});
     if (!exact || c.skinny) return run(x4, pair, a, c, s);
     // A few rows behind the last whole tile go to the skinny kernel where another
-    // round of tiles would take longer (4097 rows of 14336 x 4096, 4-bit: 159 us
-    // against 164).
+    // round of tiles would take longer (4097 4-bit rows with 4096 x 4096 take 48 us
+    // so, 65 on 128x128 tiles; 8193 with 8192 x 8192 286, 327 on 256x256 ones).
     const int64_t tail = a.g.n % kTiles[x4][c.i].nt;
     if (tail == 0 || tail > 32 || tail == a.g.n) return run(x4, pair, a, c, s);
     Mx4Args head = a, rest = a;
