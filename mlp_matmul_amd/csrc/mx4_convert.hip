@@ -10,7 +10,9 @@
 // Four lanes share a block, eight numbers each: one 16-byte load of bf16 (two
 // of fp32), the largest magnitude as an integer over the four lanes by DPP, and
 // the hardware's conversion, two numbers an instruction, which rounds and
-// saturates as above (v_cvt_scalef32_pk_fp4_*).  Memory bound.
+// saturates as above (v_cvt_scalef32_pk_fp4_*).  Memory bound: 14336 x 4096 in
+// bf16 takes 26.3 us there and 22.0 back, 149 MB each (5.7 and 6.8 TB/s; a copy
+// of 2 GiB runs at 4.85).
 #include <algorithm>
 
 #include "grouped_common.h"
