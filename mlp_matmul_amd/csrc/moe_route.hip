@@ -219,7 +219,8 @@ __device__ __forceinline__ double row_sum64(double v) {
 __device__ __forceinline__ double exp64(double x) {
     x = fmax(x, -708.0);
     const double n = rint(x * 1.4426950408889634074);
-    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.693147180369123816490, x));   // ln 2 in two parts
+    // ln 2 as the nearest double and what that leaves: the inner product is exact within its fma
+    const double r = fma(n, -2.3190468138462996e-17, fma(n, -0.6931471805599453, x));
     double y = 1.0 / 6227020800.0;
     y = fma(y, r, 1.0 / 479001600.0);
     y = fma(y, r, 1.0 / 39916800.0);

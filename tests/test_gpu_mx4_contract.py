@@ -276,3 +276,25 @@ def test_many_numbers(torch_cuda):  # noqa: F811
     assert int((m.scales != 0).any(1).sum()) == len(some)
     back = uw.mx4_dequantize(m, out=x)
     assert torch.equal(f64(back[some]), values_ref(codes, scales))
+
+
+def test_nothing_to_do(torch_cuda):  # noqa: F811
+    """No rows, no weights, no tokens."""
+    torch = torch_cuda
+    print_case("empty calls")
+    W, _ = weight(torch, 1, 48, 96)
+    none = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
+    m = uw.mx4_quantize(none)
+    assert m.shape == (0, 96) and uw.mx4_dequantize(m).shape == (0, 96)
+    for x in (none, m):
+        assert uw.linear(W, x).shape == (0, 48)
+        assert uw.gemm_grouped(W, x, torch.zeros(4, dtype=torch.int32, device="cuda")[:4]).shape == (0, 16)
+    x = normal(torch, 2, 5, 96)
+    assert uw.linear(m, x).shape == uw.linear(m, uw.mx4_quantize(x)).shape == (5, 0)
+    narrow = uw.mx4_quantize(x[:, :0])
+    assert narrow.shape == (5, 0) and uw.mx4_dequantize(narrow).shape == (5, 0)
+    r = uw.moe_route_scored(torch.empty(0, 3, device="cuda"), 2)
+    assert r.ids.shape == (0, 2) and bool((r.offsets == 0).all())
+    D, _ = weight(torch, 3, 3 * 96, 32)
+    G, _ = weight(torch, 4, 3 * 32, 96)
+    assert uw.moe_experts(G, G, D, none, r).shape == (0, 96)
