@@ -35,7 +35,7 @@ constexpr TileCost kTiles[2][MX4_TILE_SHAPES] = {      // bf16 rows, 4-bit rows
      {256, 128, 1, 1.34, 1.62, 1.52, 5.6, 5.5, 1.5}},
     {{64, 64, 4, 0.30, 0.55, 1.01, 5.0, 3.3, 1.1},
      {128, 128, 2, 0.69, 1.08, 1.24, 5.4, 4.9, 0.8},
-     {256, 256, 1, 1.25, 1.72, 1.68, 7.8, 8.0, 5.9}}};
+     {256, 256, 1, 1.25, 1.72, 1.68, 7.8, 8.0, 3.6}}};
 constexpr int kStepCols[2] = {128, 256};
 // The skinny kernel: a wave's step of 128 columns with few waves and with the
 // chip full of them; the launch, and what a workgroup needs around its steps.

@@ -155,7 +155,7 @@ __global__ __launch_bounds__(64 * KW) void mx4_skinny_kernel(Mx4Args a, uint32_t
         for (int r = 0; r < NRB; ++r) {
             if constexpr (X4) {
 #pragma unroll
-                for (int n = 0; n < NB; ++n) acc[r][n] = mfma_mx4<0>(wf[r], ws[r], xf[0][n], xs[n], acc[r][n]);
+                for (int n = 0; n < NB; ++n) acc[r][n] = mfma_mx4<0, 0>(wf[r], ws[r], xf[0][n], xs[n], acc[r][n]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

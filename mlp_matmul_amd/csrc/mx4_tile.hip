@@ -20,12 +20,13 @@
 //   bf16 rows:   64x64 1291,  128x64 1073,  256x128 861 (1.28 PFLOP/s)
 //   4-bit rows:  64x64 533,   128x128 357,  256x256 288 (3.8 PFLOP/s)
 // Small ones for few rows: 777 rows of 14336 x 4096 in bf16 take 128, 106 and 108;
-// 32 experts with 19 rows each on 1024 x 2048 pairs 47, 40 and 62.
+// 32 experts with 75 rows each on 1024 x 2048 pairs 47, 40 and 62.
 // Of the 256x256 tile's 726 thousand cycles the matrix units work 262, the LDS 213
 // on fragments and 65 on what arrives, and its loads take 143 to issue: two
-// waves a SIMD between barriers hide only part of these behind each other (without
-// loads 428; four waves with tiles of 128x128 take half as long again, and reading a
-// step or more ahead into L2 changes nothing).
+// waves a SIMD between barriers hide only part of these behind each other.  Without
+// loads it takes 428.  Four waves of 128x128 each, with twice the registers, take
+// 345 us; reading a step or more ahead into L2, loads spread among the products and
+// priorities of waves change nothing.
 #include <type_traits>
 
 #include "kernels.h"
@@ -157,8 +158,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
     struct FragsB {
         u32x4_t B[FG][BK];
     };
+    // 4-bit rows: two 16-row blocks' in a register, two bytes each (one in each, the 256x256 tile with columns behind the
+    // last step would spill 62 registers, not 34: 14336 x 4000 with 4096 rows 199 us, not 182)
     struct Scales {
-        uint32_t a[FM], b[X4 ? FN : 1];
+        uint32_t a[X4 ? FM / 2 : FM], b[X4 ? FN / 2 : 1];
     };
     auto a_block = [&](int i) { return PAIR ? (i < FM / 2 ? wm * FM / 2 + i : MT / 32 + wm * FM / 2 + i - FM / 2) : wm * FM + i; };
     // One variable index and one constant each: behind a longer chain of sums the compiler no longer knows the array,
@@ -197,13 +200,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
         asm("" : "+v"(a0));
         if (X4) asm("" : "+v"(b0));
         const uint8_t* const b = scales_of(i);
+        auto at_a = [&](int k) { return b + a0 + (PAIR && k >= FM / 2 ? MT / 32 + k - FM / 2 : k) * 256; };
+        auto at_b = [&](int k) { return b + b0 + (k / FG * (NT / 16 / G) + k % FG) * 256; };
+        auto two = [](const uint8_t* p, const uint8_t* q) {
+            const s16x2_t v{*reinterpret_cast<const int16_t*>(p), *reinterpret_cast<const int16_t*>(q)};
+            return __builtin_bit_cast(uint32_t, v);
+        };
+        if constexpr (X4) {
 #pragma unroll
-        for (int k = 0; k < FM; ++k) {
-            const uint8_t* const p = b + a0 + (PAIR && k >= FM / 2 ? MT / 32 + k - FM / 2 : k) * 256;
-            f.a[k] = X4 ? *reinterpret_cast<const uint16_t*>(p) : *p;
+            for (int k = 0; k < FM / 2; ++k) f.a[k] = two(at_a(2 * k), at_a(2 * k + 1));
+#pragma unroll
+            for (int k = 0; k < FN / 2; ++k) f.b[k] = two(at_b(2 * k), at_b(2 * k + 1));
+        } else {
+#pragma unroll
+            for (int k = 0; k < FM; ++k) f.a[k] = *at_a(k);
         }
-#pragma unroll
-        for (int k = 0; k < (X4 ? FN : 0); ++k) f.b[k] = *reinterpret_cast<const uint16_t*>(b + b0 + (k / FG * (NT / 16 / G) + k % FG) * 256);
     };
     f32x4_t acc[FM][FN];
 #pragma unroll
@@ -216,8 +227,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
         for (int i = 0; i < FM; ++i) {
             if constexpr (X4) {
 #pragma unroll
-                for (int j = 0; j < FG; ++j)
-                    acc[i][g * FG + j] = mfma_mx4<H>(fa.A[i], sc.a[i], fb.B[j][0], sc.b[g * FG + j], acc[i][g * FG + j]);
+                for (int j = 0; j < FG; ++j) {
+                    const uint32_t sa = sc.a[i / 2], sb = sc.b[(g * FG + j) / 2];
+                    f32x4_t& d = acc[i][g * FG + j];
+                    if (i % 2) d = j % 2 ? mfma_mx4<2 + H, 2 + H>(fa.A[i], sa, fb.B[j][0], sb, d) : mfma_mx4<2 + H, H>(fa.A[i], sa, fb.B[j][0], sb, d);
+                    else d = j % 2 ? mfma_mx4<H, 2 + H>(fa.A[i], sa, fb.B[j][0], sb, d) : mfma_mx4<H, H>(fa.A[i], sa, fb.B[j][0], sb, d);
+                }
             } else {
 #pragma unroll
                 for (int k = 0; k < BK; ++k) {
@@ -343,10 +358,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4Args a, ui
                 for (int i = 0; i < FM; ++i) {
                     if (X4) f.A[X4 ? i : 0] = u32x4_t{0u, 0u, 0u, 0u};
                     else f.a[X4 ? 0 : i] = u32x2_t{0u, 0u};
-                    sc.a[i] = X4 ? (h ? (sc.a[i] & 0xFFu) | 127u << 8 : 127u | 127u << 8) : 127u;
                 }
+                const uint32_t keep = X4 && h ? 0x00FF00FFu : 0u, one = (X4 ? 0x7F7F7F7Fu : 0x7Fu) & ~keep;
 #pragma unroll
-                for (int i = 0; i < (X4 ? FN : 0); ++i) sc.b[i] = h ? (sc.b[i] & 0xFFu) | 127u << 8 : 127u | 127u << 8;
+                for (int i = 0; i < (X4 ? FM / 2 : FM); ++i) sc.a[i] = (sc.a[i] & keep) | one;
+#pragma unroll
+                for (int i = 0; i < (X4 ? FN / 2 : 0); ++i) sc.b[i] = (sc.b[i] & keep) | one;
 #pragma unroll
                 for (int i = 0; i < (X4 ? 0 : FG); ++i)
 #pragma unroll
