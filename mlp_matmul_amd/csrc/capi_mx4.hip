@@ -228,12 +228,12 @@ int uw_moe_experts(int form, const void* gate, const void* up, const void* down,
         const uint16_t* w[3] = {};
         const uw_dmat* d[3] = {};
         const uw_mx4* m[3] = {};
+        uwk::Mx4Mat mats[3];
         for (int i = 0; i < 3; ++i) {
             const int64_t r = i < 2 ? rows : cols, c = i < 2 ? cols : rows;
             if (mx4) {
-                uwk::Mx4Mat probe;
                 m[i] = static_cast<const uw_mx4*>(given[i]);
-                rc = take_experts(m[i], experts, r, c, &probe, &in, who);
+                rc = take_experts(m[i], experts, r, c, &mats[i], &in, who);
             } else {
                 uwk::Weight probe;
                 if (form == UW_FORM_BF16) w[i] = static_cast<const uint16_t*>(given[i]);
@@ -264,8 +264,16 @@ int uw_moe_experts(int form, const void* gate, const void* up, const void* down,
         uint16_t* const h = reinterpret_cast<uint16_t*>(base + l.h);
         float* const y = reinterpret_cast<float*>(base + l.y);
         if (mx4) {
-            if ((rc = uw_mx4_gate_up(m[0], m[1], experts, X, tokens, ldx, nullptr, offsets, order, top_k, n, h, rows, stream)) ||
-                (rc = uw_mx4_gemm_grouped(m[2], experts, h, n, rows, nullptr, offsets, nullptr, 1, n, y, UW_F32, cols, stream)))
+            if ((rc = uw_mx4_gate_up(m[0], m[1], experts, X, tokens, ldx, nullptr, offsets, order, top_k, n, h, rows, stream)))
+                return rc;
+            if (tokens == 1) {                  // a single token's sum needs no array of the experts' outputs
+                const uwk::Mx4OneArgs a{mats[2], h, rows, offsets, place, weights, experts, top_k, int32_t(cols), int32_t(rows), ep};
+                if (uwk::mx4_one_supported(a)) {
+                    const hipError_t e = uwk::launch_mx4_one(a, as_stream(stream));
+                    return e == hipSuccess ? UW_OK : hip_fail(e, who);
+                }
+            }
+            if ((rc = uw_mx4_gemm_grouped(m[2], experts, h, n, rows, nullptr, offsets, nullptr, 1, n, y, UW_F32, cols, stream)))
                 return rc;
         } else {
             void* const room = base + l.total;

@@ -34,6 +34,20 @@ hipError_t launch_mx4_dequantize(const Mx4Mat& m, int64_t rows, int64_t cols, vo
 // The product of any shape (x4: the rows of X are 4-bit too).
 hipError_t launch_mx4(bool x4, bool pair, const Mx4Args& a, hipStream_t s);
 
+// A single token's down projection with the sum over its experts.
+struct Mx4OneArgs {
+    Mx4Mat w;                   // [E*R, C]
+    const uint16_t* h;          // top_k rows of C, ldh apart
+    int64_t ldh;
+    const int32_t* offsets;
+    const int32_t* place;
+    const float* weights;
+    int32_t E, top_k, R, C;
+    Epilogue ep;
+};
+bool mx4_one_supported(const Mx4OneArgs& a);                  // and faster
+hipError_t launch_mx4_one(const Mx4OneArgs& a, hipStream_t s);
+
 // The kernels behind it.  Up to `rows` (4, 16 or 32; 16 or 32 4-bit ones) rows an expert before its weights are read
 // again.
 hipError_t launch_mx4_skinny(bool x4, bool pair, const Mx4Args& a, int rows, hipStream_t s);

@@ -171,6 +171,53 @@ def test_experts(torch_cuda, form, tokens, experts, top_k, groups, top_groups, F
     assert torch.equal(y, out), what
 
 
+@pytest.mark.parametrize("E,k,F,H", [(1, 1, 32, 32), (8, 2, 160, 96), (130, 16, 64, 256), (70, 16, 32, 2080), (6, 3, 4128, 2496),
+                                     (512, 4, 96, 544), (6, 3, 4128, 32), (2, 2, 192, 64)])
+def test_one_token(torch_cuda, E, k, F, H):
+    """Its experts are summed in the down projection's kernel, or where sums are long in one of their own; also with
+    slots that have no expert."""
+    torch = torch_cuda
+    print_case(f"one token, {k} of {E} experts of {F}x{H}")
+    ws, vs = three_weights(torch, "mx4", E, F, H, E)
+    X = torch.randn(1, H, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    l = logits_of(torch, 8, 1, E)
+    for some in (E, max(1, k - 1)):
+        l[0, some:] = -float("inf")
+        r = uw.moe_route_scored(l, k, scale=1.5)
+        assert int((r.ids >= 0).sum()) == min(k, some)
+        for residual, kind in ((None, torch.float32), (X, torch.bfloat16)):
+            out = uw.moe_experts(*ws, X, r, residual=residual, out_dtype=kind)
+            want, err = experts_ref(torch, f64(X), vs, r.ids.cpu(), f64(r.weights), residual)
+            limit = err + (want.abs() + err) * (torch.finfo(kind).eps / 2) + 1e-30
+            assert not bool(((f64(out) - want).abs() > limit).any())
+    l[:] = -float("inf")
+    r = uw.moe_route_scored(l, k)
+    assert torch.equal(uw.moe_experts(*ws, X, r, residual=X), X.float())
+    assert not bool(uw.moe_experts(*ws, X, r).any())
+
+
+def test_one_token_on_a_bad_routing(torch_cuda):
+    """Places and offsets that no router returns: nothing outside is read, slots whose row no expert holds count nothing."""
+    torch = torch_cuda
+    print_case("one token, bad routing")
+    E, k, F, H = 5, 4, 96, 160
+    ws, vs = three_weights(torch, "mx4", E, F, H, 2)
+    X = torch.randn(1, H, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+
+    def made(offsets, place):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        return uw.Routing(None, torch.tensor([[0.5, 0.25, 1.0, 2.0]], device="cuda"), torch.tensor(offsets, **i32),
+                          torch.arange(4, **i32), torch.tensor([place], **i32))
+
+    # rows 0 and 1 of expert 1, row 2 of expert 3
+    r = made([0, 0, 2, 2, 3, 3], [1, 2 ** 31 - 1, -7, 2])
+    want, err = experts_ref(torch, f64(X), vs, torch.tensor([[1, -1, -1, 3]]), f64(r.weights), None)
+    out = uw.moe_experts(*ws, X, r)
+    assert bool(((f64(out) - want).abs() <= err + (want.abs() + err) * 2.0 ** -24).all())
+    for offsets in ([0, 9, -4, 2 ** 31 - 1, 1, 0], [4, 3, 2, 1, 0, -1], [-2 ** 31] * 6, [2 ** 31 - 1] * 6):
+        assert uw.moe_experts(*ws, X, made(offsets, [0, 1, 2, 3])).shape == (1, H)
+
+
 @pytest.mark.parametrize("form", ["bf16", "palette"])
 def test_experts_is_the_layer(torch_cuda, form):
     """On moe_route's routing the result is moe_layer's, bit for bit (from two tokens on)."""

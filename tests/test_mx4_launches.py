@@ -75,6 +75,22 @@ def test_the_experts_are_three_products_and_a_sum(recorder):  # noqa: F811
     assert names[0].startswith("mx4_") and names[1].startswith("mx4_") and names[2].startswith("combine_kernel"), names
 
 
+def test_one_token_sums_its_experts_in_one_kernel(recorder):  # noqa: F811
+    """Where sums are not too long for the rows."""
+    L = recorder.lib
+
+    def names(rows, cols):
+        rcs = []
+        seen = recorder.launches(lambda: rcs.append(L.uw_moe_experts(
+            2, matrix(1, 4 * rows, cols), matrix(3, 4 * rows, cols), matrix(5, 4 * cols, rows), 4, rows, cols, at(7), cols, 1, 2,
+            at(8), at(9), at(10), at(11), None, 0, 0, at(13), 1, cols, at(14), 1 << 24, None)))
+        assert rcs == [0], L.uw_last_error()
+        return [k.split("<")[0] for k, *_ in seen]
+
+    assert names(160, 64) == names(32, 96) == ["mx4_skinny_kernel", "mx4_one_kernel"]
+    assert names(192, 64) == ["mx4_skinny_kernel", "mx4_skinny_kernel", "combine_kernel"]
+
+
 def test_more_numbers_than_a_launch_takes(recorder):  # noqa: F811
     """2^32 - 1 eights of numbers a launch: the rest of the rows follow, where the first ones end."""
     L, rows, cols = recorder.lib, (1 << 21) + 5, 1 << 15
