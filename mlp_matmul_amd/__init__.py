@@ -419,17 +419,18 @@ class Routing(NamedTuple):
 
 def _value_type(t, name):
     torch = _torch()
-    if t.dtype == torch.float32:
+    kind = getattr(t, "dtype", None)                         # a compressed or 4-bit matrix has none
+    if kind == torch.float32:
         return UW_F32
-    if t.dtype == torch.bfloat16:
+    if kind == torch.bfloat16:
         return UW_BF16
-    raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+    raise ValueError(f"{name} must be float32 or bfloat16, not {kind or type(t).__name__}")
 
 
 def _matrix_arg(t, name, rows=None, cols=None):
     """Row stride of a 2-D tensor whose rows are contiguous."""
-    if isinstance(t, Mx4Matrix):
-        raise ValueError(f"{name} cannot be an Mx4Matrix here")
+    if isinstance(t, (Mx4Matrix, DeviceMatrix)):
+        raise ValueError(f"{name} cannot be a matrix of the type {type(t).__name__} here")
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}], "
                          f"not {list(t.shape)}")
@@ -441,8 +442,8 @@ def _matrix_arg(t, name, rows=None, cols=None):
 def _x_arg(X, cols=None):
     if isinstance(X, Mx4Matrix):
         raise ValueError("X must be bfloat16: only products with Mx4Matrix weights, but moe_experts, take it as an Mx4Matrix")
-    if X.dtype != _torch().bfloat16:
-        raise ValueError(f"X must be bfloat16, not {X.dtype}")
+    if getattr(X, "dtype", None) != _torch().bfloat16:
+        raise ValueError(f"X must be bfloat16, not {getattr(X, 'dtype', type(X).__name__)}")
     ld = _matrix_arg(X, "X", None, cols)
     return ld if X.shape[0] > 1 else (X.shape[1] + 7) // 8 * 8
 
@@ -556,15 +557,17 @@ def _out_arg(out, rows, cols, dtype, dev):
         dtype = dtype or torch.float32
         out = _new_matrix(rows, cols, dtype, dev)
         return out, max(cols, 1), _value_type(out, "out")
+    kind = _value_type(out, "out")
     if dtype is not None and out.dtype != dtype:
         raise ValueError(f"out is {out.dtype}, out_dtype {dtype}")
-    return out, _matrix_arg(out, "out", rows, cols), _value_type(out, "out")
+    return out, _matrix_arg(out, "out", rows, cols), kind
 
 
 def _residual_arg(residual, rows, cols):
     if residual is None:
         return None, UW_F32, 0
-    return residual.data_ptr(), _value_type(residual, "residual"), _matrix_arg(residual, "residual", rows, cols)
+    kind = _value_type(residual, "residual")
+    return residual.data_ptr(), kind, _matrix_arg(residual, "residual", rows, cols)
 
 
 def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None, scratch=None, stream=None):
@@ -590,21 +593,22 @@ def linear(W, X, bias=None, act="none", residual=None, out=None, out_dtype=None,
     else:
         w, d, rows, cols = _weight_arg(W, None)
         ldx, batch = _x_arg(X, cols), X.shape[0]
+    bias_type = UW_F32 if bias is None else _value_type(bias, "bias")
     if bias is not None and (bias.dim() != 1 or bias.shape[0] != rows or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous [{rows}] tensor")
     res, res_type, ldr = _residual_arg(residual, batch, rows)
     out, ldo, out_type = _out_arg(out, batch, rows, out_dtype, dev)
     if mx4:
         check(lib().uw_mx4_linear(ct.byref(W.mx4), xp, ldx, x4, batch, None if bias is None else bias.data_ptr(),
-                                  UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type,
-                                  ldr, out.data_ptr(), out_type, ldo, _current_stream(dev)), "uw_mx4_linear")
+                                  bias_type, ACTIVATIONS[act], res, res_type, ldr, out.data_ptr(), out_type, ldo,
+                                  _current_stream(dev)), "uw_mx4_linear")
         return out
     if scratch is None and batch > 2:                        # never any through 2 rows
         need = lib().uw_linear_scratch_bytes(0 if d is None else 1, rows, cols, batch)
         scratch = _new_scratch(need, 0, dev)
     sp, sb = _scratch_arg(scratch)
     check(lib().uw_linear(w, d, rows, cols, X.data_ptr(), ldx, batch, None if bias is None else bias.data_ptr(),
-                          UW_F32 if bias is None else _value_type(bias, "bias"), ACTIVATIONS[act], res, res_type, ldr,
+                          bias_type, ACTIVATIONS[act], res, res_type, ldr,
                           out.data_ptr(), out_type, ldo, sp, sb, _current_stream(dev)), "uw_linear")
     return out
 
@@ -660,7 +664,8 @@ def moe_route_scored(logits, top_k, score="sigmoid", bias=None, groups=1, top_gr
         raise ValueError(f"score must be one of {sorted(SCORES)}")
     ld, kind = _matrix_arg(logits, "logits"), _value_type(logits, "logits")
     tokens, experts = logits.shape
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (experts,) or not bias.is_contiguous()):
+    if bias is not None and (getattr(bias, "dtype", None) != torch.float32 or tuple(bias.shape) != (experts,) or
+                             not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 [{experts}] tensor")
     r, scratch = _routing(tokens, experts, top_k, scratch, dev)
     sp, sb = _scratch_arg(scratch)
@@ -768,7 +773,7 @@ def moe_combine(Y, place, weights, residual=None, out=None, out_dtype=None, stre
         with ctx:
             return moe_combine(Y, place, weights, residual, out, out_dtype)
     torch = _torch()
-    if Y.dtype != torch.float32 or Y.dim() != 2 or not Y.is_contiguous():
+    if getattr(Y, "dtype", None) != torch.float32 or Y.dim() != 2 or not Y.is_contiguous():
         raise ValueError("Y must be a contiguous float32 [rows, cols] tensor")
     if place.dim() != 2:
         raise ValueError("place must be [tokens, top_k]")
@@ -902,6 +907,8 @@ def mx4_quantize(X, out=None, stream=None) -> Mx4Matrix:
         raise ValueError(f"X must have a multiple of 32 columns, not {cols}")
     if out is None:
         out = Mx4Matrix._empty(rows, cols, dev)
+    elif not isinstance(out, Mx4Matrix):
+        raise ValueError(f"out must be an Mx4Matrix, not {type(out).__name__}")
     elif out.shape != (rows, cols):
         raise ValueError(f"out must be [{rows}, {cols}], not {list(out.shape)}")
     m = out.mx4

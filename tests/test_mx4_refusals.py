@@ -308,6 +308,38 @@ def test_python_refusals(on_gpu):
                 call()
 
 
+def test_a_matrix_in_the_place_of_a_tensor(on_gpu):
+    """A 4-bit matrix where a call takes a tensor, and a tensor where it takes a 4-bit matrix to write, are refused as
+    other arguments of a wrong type are."""
+    W, X, M = on_gpu(128, 96), Bf16(4, 96), on_gpu(4, 128)
+    f32, i32 = torch.float32, torch.int32
+    off, order = Bf16(5, dtype=i32), Bf16(40, dtype=i32)
+    D = uw.DeviceMatrix.__new__(uw.DeviceMatrix)
+    D.info, D.buffers = uw.uw_info(rows=4, cols=96), {"nib": OnGpu()}
+    with torch.no_grad():
+        for call, match in (
+                (lambda: uw.mx4_quantize(X, out=Bf16(4, 96)), "out must be an Mx4Matrix"),
+                (lambda: uw.mx4_quantize(X, out=D), "out must be an Mx4Matrix"),
+                (lambda: uw.mx4_quantize(D), "X"),
+                (lambda: uw.mx4_dequantize(M, out=M), "out"),
+                (lambda: uw.mx4_dequantize(M, out=M, out_dtype=f32), "out"),
+                (lambda: uw.linear(W, X, out=M), "out"),
+                (lambda: uw.linear(W, X, out=M, out_dtype=f32), "out"),
+                (lambda: uw.linear(W, X, residual=M), "residual"),
+                (lambda: uw.linear(W, X, residual=D), "residual"),
+                (lambda: uw.linear(W, X, bias=M), "bias"),
+                (lambda: uw.linear(W, D), "X"),
+                (lambda: uw.gemm_grouped(W, X, off, order, 2, out=on_gpu(40, 32)), "out"),
+                (lambda: uw.gemm_grouped(W, X, off, order, 2, out=on_gpu(40, 32), out_dtype=f32), "out"),
+                (lambda: uw.moe_gate_up(W, W, X, off, order, 2, h=on_gpu(40, 32)), "out|h "),
+                (lambda: uw.moe_combine(M, Bf16(4, 2, dtype=i32), Bf16(4, 2, dtype=f32)), "Y must be"),
+                (lambda: uw.moe_combine(Bf16(8, 96, dtype=f32), Bf16(4, 2, dtype=i32), Bf16(4, 2, dtype=f32), residual=M),
+                 "residual"),
+                (lambda: uw.moe_route_scored(Bf16(4, 8, dtype=f32), 2, bias=M), "bias must be")):
+            with pytest.raises(ValueError, match=match):
+                call()
+
+
 def test_moe_experts_refusals(on_gpu):
     i32 = torch.int32
 
