@@ -176,6 +176,27 @@ def test_linear_every_weight(torch_cuda, x4):
         assert bool(((got - w[:, at].t()).abs()[:, ~bad] <= 2.0 ** -125).all())
 
 
+@pytest.mark.parametrize("x4", [False, True])
+def test_linear_smallest_weights(torch_cuda, x4):
+    """One-hot rows on scale bytes 0 to 3: weights of 2^-126 and above come back as they are; those below, which fp32 holds
+    as subnormal numbers, as they are or as zero."""
+    torch = torch_cuda
+    rows, cols = 80, 352
+    W, _ = weight(torch, 12, rows, cols)
+    W.scales[:] = torch.arange(11, dtype=torch.uint8, device="cuda") % 4
+    w = values_ref(W.codes, W.scales)
+    for batch in (1, 3, 16, 40, 352):
+        print_case(f"mx4 one-hot, smallest scales, {batch} x4={x4}")
+        at = torch.arange(batch) * 37 % cols
+        X = torch.zeros(batch, cols, dtype=torch.bfloat16)
+        X[torch.arange(batch), at] = 1.0
+        X = X.cuda()
+        got, want = f64(uw.linear(W, uw.mx4_quantize(X) if x4 else X)), w[:, at].t()
+        small = want.abs() < 2.0 ** -126
+        assert 0 < int(small.sum()) < small.numel()
+        assert bool(((got == want) | (small & (got == 0))).all())
+
+
 def test_linear_numbers_that_are_none(torch_cuda):
     """A NaN or an infinity of a row of X stays in that row."""
     torch = torch_cuda

@@ -81,6 +81,33 @@ def test_ties_and_padding(torch_cuda, score):
                         bias=b, groups=groups, top_groups=top_groups, group_top=group_top, renormalize=groups != 6)
 
 
+@pytest.mark.parametrize("experts,groups", [(40, 10), (64, 16), (128, 16), (128, 2), (200, 5), (256, 8), (256, 4), (512, 16), (512, 8)])
+def test_group_ties(torch_cuda, experts, groups):
+    """Groups whose keys are equal, among them those of experts 64 apart and more, and groups of a few experts: the lowest
+    index goes first.  Few different logits, so that most keys are equal."""
+    torch = torch_cuda
+    inf = float("inf")
+    g = torch.Generator().manual_seed(experts + groups)
+    per = experts // groups
+    l = torch.randint(-1, 2, (220, experts), generator=g).float()
+    l[0] = 1.0
+    l[1] = -200.0
+    l[2, :experts - per] = -inf                            # the last group alone
+    l[3] = torch.arange(experts).flip(0).float() / experts
+    l[4:40][torch.rand(36, experts, generator=g) < 0.9] = -inf
+    l[40:80, ::per] = 2.0                                  # every group's best key is the same
+    l[219] = -inf
+    bias = torch.randint(-1, 2, (experts,), generator=g).float() * 0.25
+    for score in ("sigmoid", "softmax"):
+        for group_top in (1, 2):
+            for b in (None, bias.cuda()):
+                for top_groups in sorted({1, groups // 2, groups - 1}):
+                    for tokens in (9, 220):
+                        compare(torch, l[:tokens].cuda(), min(6, top_groups * per),
+                                f"group ties {experts}/{groups} top {top_groups} of {group_top} {score} bias={b is not None} {tokens}",
+                                score=score, bias=b, groups=groups, top_groups=top_groups, group_top=group_top)
+
+
 def test_neighbouring_scores(torch_cuda):
     """Logits one step of fp32 apart, and far tails: which score is larger after its rounding decides."""
     torch = torch_cuda
