@@ -52,6 +52,13 @@ hipError_t launch_mx4_one(const Mx4OneArgs& a, hipStream_t s);
 // again.
 hipError_t launch_mx4_skinny(bool x4, bool pair, const Mx4Args& a, int rows, hipStream_t s);
 int mx4_skinny_waves(int rows, const Mx4Args& a);             // of its workgroups
+// Steps of a wave on their way: four where LDS has room (one row with 4096 x 14336 takes 8.8 us so, 9.5 with two); and the
+// workgroup's LDS in KB, slots of a step of the weights and rows, and the scales.
+constexpr int mx4_skinny_depth(int rows, int waves) { return rows == 4 && waves == 8 ? 4 : 2; }
+constexpr int mx4_skinny_lds(bool x4, bool pair, int rows, int waves) {
+    const int w = pair ? 2 : 1, x = x4 ? (rows + 15) / 16 : rows / 4;
+    return waves * ((w + x) * mx4_skinny_depth(rows, waves) + w + (x4 ? x : 0));
+}
 // Tiles of weight rows x input rows.
 enum Mx4TileShape { MX4_TILE_SMALL, MX4_TILE_MIDDLE, MX4_TILE_LARGE, MX4_TILE_SHAPES };
 hipError_t launch_mx4_tile(bool x4, bool pair, const Mx4Args& a, Mx4TileShape shape, hipStream_t s);

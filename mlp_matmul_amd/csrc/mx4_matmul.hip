@@ -77,10 +77,8 @@ double tile_us(const Problem& p, int i) {
 
 double skinny_us(const Problem& p, int i) {
     const SkinnyCost& c = kSkinny[p.x4][p.pair][i];
-    const int rows = kSkinnyRows[i], kw = mx4_skinny_waves(rows, p.a), m = p.pair ? 2 : 1;
-    const int x = p.x4 ? std::max(1, rows / 16) : rows / 4, depth = rows == 4 && kw == 8 ? 4 : 2;
-    const int lds = kw * ((m + x) * depth + m + (p.x4 ? x : 0));           // KB
-    const int per_cu = std::max(1, std::min(160 / lds, 32 / kw));
+    const int rows = kSkinnyRows[i], kw = mx4_skinny_waves(rows, p.a);
+    const int per_cu = std::max(1, std::min(160 / mx4_skinny_lds(p.x4, p.pair, rows, kw), 32 / kw));
     const double tiles = p.tiles(rows), rounds = p.groups * double((p.a.g.R + 15) / 16) * tiles / p.a.g.cus / per_cu;
     const double step = c.few + (c.full - c.few) * std::min(1.0, rounds);
     return c.launch + std::max(std::max(1.0, rounds) * (std::max(1.0, double(p.a.g.C) / 128 / kw) * step + c.around), p.stream_us(tiles));

@@ -44,6 +44,8 @@ __global__ __launch_bounds__(64 * KW) void mx4_skinny_kernel(Mx4Args a, uint32_t
     static_assert(NRB * NB * 1024 <= kSlot, "partial sums fit the first slots");
     // an array per slot: the compiler can tell them apart
     constexpr int kRing = KW * kSlot;
+    static_assert(D == mx4_skinny_depth(NT, KW) && D * kRing + KW * SB * 1024 == mx4_skinny_lds(X4, PAIR, NT, KW) * 1024,
+                  "what the choice of a kernel counts with");
     __shared__ __align__(16) uint8_t ring0[kRing], ring1[kRing], ring2[D > 2 ? kRing : 16], ring3[D > 3 ? kRing : 16];
     __shared__ __align__(16) uint8_t scale_buf[KW * SB * 1024];
 
@@ -259,11 +261,11 @@ hipError_t launch(const Mx4Args& a, hipStream_t s) {
 template <bool X4, bool PAIR, int NT>
 hipError_t launch_nt(const Mx4Args& a, hipStream_t s) {
     constexpr int R = PAIR ? 2 : 1;
+    constexpr int most = NT > 16 ? 4 : 8;
     switch (mx4_skinny_waves(NT, a)) {
-        case 2: return launch<X4, PAIR, R, NT, 2, 2>(a, s);
-        case 4: return launch<X4, PAIR, R, NT, 4, 2>(a, s);
-        // four steps on their way where LDS has room: one row with 4096 x 14336 takes 8.8 us so, 9.5 with two
-        default: return launch<X4, PAIR, R, NT, (NT > 16 ? 4 : 8), (NT > 4 ? 2 : 4)>(a, s);
+        case 2: return launch<X4, PAIR, R, NT, 2, mx4_skinny_depth(NT, 2)>(a, s);
+        case 4: return launch<X4, PAIR, R, NT, 4, mx4_skinny_depth(NT, 4)>(a, s);
+        default: return launch<X4, PAIR, R, NT, most, mx4_skinny_depth(NT, most)>(a, s);
     }
 }
 
