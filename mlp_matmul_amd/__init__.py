@@ -428,9 +428,7 @@ def _value_type(t, name):
 
 
 def _matrix_arg(t, name, rows=None, cols=None):
-    """Row stride of a 2-D tensor whose rows are contiguous."""
-    if isinstance(t, (Mx4Matrix, DeviceMatrix)):
-        raise ValueError(f"{name} cannot be a matrix of the type {type(t).__name__} here")
+    """Row stride of a 2-D tensor whose rows are contiguous (its type is checked before: no other matrix comes here)."""
     if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}], "
                          f"not {list(t.shape)}")
@@ -440,9 +438,9 @@ def _matrix_arg(t, name, rows=None, cols=None):
 
 
 def _x_arg(X, cols=None):
-    if isinstance(X, Mx4Matrix):
-        raise ValueError("X must be bfloat16: only products with Mx4Matrix weights, but moe_experts, take it as an Mx4Matrix")
     if getattr(X, "dtype", None) != _torch().bfloat16:
+        if isinstance(X, Mx4Matrix):
+            raise ValueError("X must be bfloat16: only products with Mx4Matrix weights, but moe_experts, take it as an Mx4Matrix")
         raise ValueError(f"X must be bfloat16, not {getattr(X, 'dtype', type(X).__name__)}")
     ld = _matrix_arg(X, "X", None, cols)
     return ld if X.shape[0] > 1 else (X.shape[1] + 7) // 8 * 8
@@ -474,14 +472,14 @@ def _index_arg(t, name, shape):
 
 def _weight_arg(W, experts, name="W"):
     """(bf16 pointer, descriptor, rows, cols) of one expert's matrix."""
-    if isinstance(W, Mx4Matrix):
-        raise ValueError(f"{name} is an Mx4Matrix and the other weights are not")
     if isinstance(W, DeviceMatrix):
         n = experts or 1
         if W.rows % n:
             raise ValueError(f"{name}: {W.rows} rows are not {n} experts' matrices")
         return None, ct.byref(W.dmat), W.rows // n, W.cols
-    if W.dtype != _torch().bfloat16 or not W.is_contiguous():
+    if getattr(W, "dtype", None) != _torch().bfloat16 or not W.is_contiguous():
+        if isinstance(W, Mx4Matrix):
+            raise ValueError(f"{name} is an Mx4Matrix and the other weights are not")
         raise ValueError(f"{name} must be a contiguous bfloat16 tensor or a DeviceMatrix")
     if W.dim() != (2 if experts is None else 3) or (experts is not None and W.shape[0] != experts):
         raise ValueError(f"{name} must be " + ("[rows, cols]" if experts is None else f"[{experts}, rows, cols]") +
@@ -636,7 +634,7 @@ def moe_route(logits, top_k, renormalize=True, scratch=None, stream=None) -> Rou
     if ctx is not None:
         with ctx:
             return moe_route(logits, top_k, renormalize, scratch)
-    ld, kind = _matrix_arg(logits, "logits"), _value_type(logits, "logits")
+    kind, ld = _value_type(logits, "logits"), _matrix_arg(logits, "logits")
     tokens, experts = logits.shape
     r, scratch = _routing(tokens, experts, top_k, scratch, dev)
     sp, sb = _scratch_arg(scratch)
@@ -662,7 +660,7 @@ def moe_route_scored(logits, top_k, score="sigmoid", bias=None, groups=1, top_gr
     torch = _torch()
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    ld, kind = _matrix_arg(logits, "logits"), _value_type(logits, "logits")
+    kind, ld = _value_type(logits, "logits"), _matrix_arg(logits, "logits")
     tokens, experts = logits.shape
     if bias is not None and (getattr(bias, "dtype", None) != torch.float32 or tuple(bias.shape) != (experts,) or
                              not bias.is_contiguous()):
@@ -810,10 +808,10 @@ def moe_layer(gate, up, down, X, logits, top_k, renormalize=True, residual=None,
     if ctx is not None:
         with ctx:
             return moe_layer(gate, up, down, X, logits, top_k, renormalize, residual, out, out_dtype, scratch)
-    if any(isinstance(m, Mx4Matrix) for m in (gate, up, down)):
+    if isinstance(gate, Mx4Matrix):
         raise ValueError("moe_layer takes no Mx4Matrix: moe_route and moe_experts do its work with them")
     tokens, experts = X.shape[0], logits.shape[-1]
-    ldl, kind = _matrix_arg(logits, "logits", tokens), _value_type(logits, "logits")
+    kind, ldl = _value_type(logits, "logits"), _matrix_arg(logits, "logits", tokens)
     gw, gd, F, H = _weight_arg(gate, experts, "gate")
     uw_, ud, urows, ucols = _weight_arg(up, experts, "up")
     dw, dd, drows, dcols = _weight_arg(down, experts, "down")
@@ -901,7 +899,7 @@ def mx4_quantize(X, out=None, stream=None) -> Mx4Matrix:
     if ctx is not None:
         with ctx:
             return mx4_quantize(X, out)
-    ld, kind = _matrix_arg(X, "X"), _value_type(X, "X")
+    kind, ld = _value_type(X, "X"), _matrix_arg(X, "X")
     rows, cols = X.shape
     if cols % 32:
         raise ValueError(f"X must have a multiple of 32 columns, not {cols}")

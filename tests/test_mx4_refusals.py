@@ -335,7 +335,12 @@ def test_a_matrix_in_the_place_of_a_tensor(on_gpu):
                 (lambda: uw.moe_combine(M, Bf16(4, 2, dtype=i32), Bf16(4, 2, dtype=f32)), "Y must be"),
                 (lambda: uw.moe_combine(Bf16(8, 96, dtype=f32), Bf16(4, 2, dtype=i32), Bf16(4, 2, dtype=f32), residual=M),
                  "residual"),
-                (lambda: uw.moe_route_scored(Bf16(4, 8, dtype=f32), 2, bias=M), "bias must be")):
+                (lambda: uw.moe_route_scored(Bf16(4, 8, dtype=f32), 2, bias=M), "bias must be"),
+                (lambda: uw.moe_route_scored(M, 2), "logits must be"),
+                (lambda: uw.moe_route(M, 2), "logits must be"),
+                (lambda: uw.moe_layer(Bf16(4, 32, 64), W, Bf16(4, 64, 32), Bf16(4, 64), Bf16(4, 4), 2), "up is an Mx4Matrix"),
+                (lambda: uw.moe_layer(Bf16(4, 32, 64), Bf16(4, 32, 64), W, Bf16(4, 64), Bf16(4, 4), 2), "down is an Mx4Matrix"),
+                (lambda: uw.moe_layer(Bf16(4, 32, 64), Bf16(4, 32, 64), Bf16(4, 64, 32), Bf16(4, 64), M, 2), "logits must be")):
             with pytest.raises(ValueError, match=match):
                 call()
 
