@@ -599,9 +599,12 @@ int uw_mx4_gate_up(const uw_mx4* gate, const uw_mx4* up, int experts,
 
 /* uw_moe_layer behind a routing that either router made: gate/up, down on the
  * bf16 h, and the weighted sum, out[t] = sum_j weights[t][j] down_e(h_tj) +
- * residual[t].  gate, up, down: bf16 matrices, uw_dmat or uw_mx4, by `form`; of
- * uw_mx4 rows and cols are multiples of 32.  offsets, order and place as the
- * routers return them for tokens * top_k slots; out may be X or the residual.
+ * residual[t].  h is rounded to bf16 in every form, as uw_moe_layer's.  gate, up,
+ * down: bf16 matrices, uw_dmat or uw_mx4, by `form`; of uw_mx4 rows and cols are
+ * multiples of 32.  offsets, order and place as the routers return them for
+ * tokens * top_k slots; out may be X or the residual.  On bf16 weights and
+ * uw_dmat the kernels are uw_moe_layer's but for a single token's down product
+ * and sum, two launches here and one there, whose results agree to rounding.
  * scratch: uw_moe_experts_scratch_bytes() bytes (with UW_FORM_COMPRESSED those
  * that UW_FORM_BF16 asks for do too, see uw_gemm_grouped); calls that share it
  * must be ordered. */

@@ -209,7 +209,9 @@ class Mx4Matrix:
     [rows, cols/2] and scales uint8 [rows, cols/32], the rows of each contiguous
     and a multiple of 16 bytes apart.  The matrices of a layer's experts are one
     matrix of experts*rows rows.  The tensors are kept, not copied; their addresses are
-    taken once, so they are not to be resized or moved."""
+    taken once, so they are not to be resized or moved.  Scales of other rows, as of
+    1408 columns, go into such ones first: with n = scales.shape[1],
+    torch.nn.functional.pad(scales, (0, -n % 16))[:, :n]."""
 
     requires_grad = False              # as a tensor's
 
@@ -842,9 +844,9 @@ def moe_experts(gate, up, down, X, routing, residual=None, out=None, out_dtype=N
     """uw_moe_experts: moe_layer's sum over each token's experts (+ residual) on
     a Routing that moe_route or moe_route_scored returned.  gate, up and down as
     moe_layer's, or all three Mx4Matrix of experts*F, experts*F and experts*H
-    rows; `out` may be X or the residual.  `scratch` (None: allocated) needs
-    moe_experts_scratch_bytes() bytes; for DeviceMatrix weights those of
-    UW_FORM_BF16 do too, and prompts are slower."""
+    rows; `out` may be X or the residual.  h, between up and down, is rounded to
+    bf16.  `scratch` (None: allocated) needs moe_experts_scratch_bytes() bytes; for
+    DeviceMatrix weights those of UW_FORM_BF16 do too, and prompts are slower."""
     ids, weights, offsets, order, place = routing
     dev = _one_device(X, gate, up, down, weights, offsets, order, place, residual, out, scratch)
     ctx = _elsewhere(dev, stream)

@@ -66,6 +66,10 @@ struct ExpertsLayout {
 
 ExpertsLayout experts_layout(int form, int experts, int64_t n, int64_t F, int64_t H) {
     ExpertsLayout l{};
+    // bf16, as uw_moe_layer's: the type that the instructions which multiply it with bf16, compressed or 4-bit weights
+    // take.  At most half a step, 2^-8, of each h, 0.0017 of the experts' sum in the norm: next to a residual and with
+    // a bf16 output the error against 64 bits is 0.0018 for one token of 6 of 64 experts (0.0017 with h in fp32) and
+    // 0.0019 for 600 tokens of 4 of 32 (0.0016)
     l.h = 0;
     l.y = align256(uint64_t(n) * uint64_t(F) * 2);
     l.total = l.y + align256(uint64_t(n) * uint64_t(H) * 4);

@@ -28,9 +28,10 @@
 // Measured: 8 tokens of 64 experts 4.1 us, a launch; 16384 of 256 12 us for the
 // selection, bound by vector instructions (85 a round of four tokens), and 8 for the
 // places, bound by the latency of a chain of small steps.  By scores: 16 tokens of
-// 64 experts 5.9 us; 16384 of 256 in 8 groups 24 for the selection, a third of it
+// 64 experts 5.8 us; 16384 of 256 in 8 groups 24 for the selection, a third of it
 // the scores' 64-bit exponentials (which every logit needs: two scores may be a
-// step apart).
+// step apart).  Workgroups of 1024 threads leave a thread 128 registers: by scores 22 of
+// them spill at 256 experts and 131 at 512, by logits none and 46.
 #include <float.h>
 
 #include <algorithm>
@@ -380,7 +381,7 @@ __device__ void select_scored(const RouteArgs& a, int64_t t, uint32_t sub, uint3
         const float l = a.type == VT_F32 ? static_cast<const float*>(a.logits)[o] : bf16_value(static_cast<const uint16_t*>(a.logits)[o]);
         w = a.score == SCORE_SIGMOID ? sigmoid_of(l) : softmax_of(fminf(l, FLT_MAX), top, scale);
     }
-    if (a.renorm) {
+    if (a.renorm) {                                        // fp32: nothing is chosen by it (5.3e-8 off in the norm, 3.4e-8 in 64 bits)
         const float all = row_sum(w);
         w = all > 0.f ? w / all : 0.f;                     // every chosen score may be 0
     }

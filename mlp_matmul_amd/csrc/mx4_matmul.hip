@@ -18,8 +18,14 @@ namespace {
 // The choice goes by estimated times, in us.  The constants are fitted to 1121
 // sizes (one matrix of 64 x 256 to 16000 x 14336 with 1 to 9000 rows, the pair
 // and the single product of 2 to 64 experts), each timed on MI355X with every
-// kernel; what the estimates choose there takes 1.01 times the fastest kernel's
-// time in the geometric mean and 1.34 times at worst.
+// kernel, so that the sum of the squared logarithms of estimate over time is least;
+// what the estimates chose there took 1.01 times the fastest kernel's time in the
+// geometric mean and 1.34 times at worst.  At 600 other sizes, drawn alike and with
+// the kernels as they are, it takes 1.034 times in the geometric mean (1.10 at the
+// 90th percentile, where two runs differ by 5 %).  The estimates are furthest
+// off for thousands of rows with a matrix of under 200 (5457 bf16 rows of 144 x
+// 1216: 26 us, 13 on 64x64 tiles) and, elsewhere, for 840 rows of pairs of five
+// experts of 3232 x 3840 (106 us, 67 on 128x64 tiles).
 //
 // Tiles: a step of a round of workgroups with one here and there, with one on
 // each compute unit, with `per_cu` on each; the launch, and what a round needs
@@ -114,7 +120,7 @@ hipError_t launch_mx4(bool x4, bool pair, const Mx4Args& a, hipStream_t s) {
     if (!exact || c.skinny) return run(x4, pair, a, c, s);
     // A few rows behind the last whole tile go to the skinny kernel where another
     // round of tiles would take longer (4097 4-bit rows with 4096 x 4096 take 48 us
-    // so, 65 on 128x128 tiles; 8193 with 8192 x 8192 286, 327 on 256x256 ones).
+    // so, 65 on 128x128 tiles; 8193 with 8192 x 8192 299, 336 on 256x256 ones).
     const int64_t tail = a.g.n % kTiles[x4][c.i].nt;
     if (tail == 0 || tail > 32 || tail == a.g.n) return run(x4, pair, a, c, s);
     Mx4Args head = a, rest = a;

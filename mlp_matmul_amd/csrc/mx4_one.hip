@@ -10,8 +10,8 @@
 // sums are added in wave order: results do not depend on scheduling.
 //
 // Bound by the launch and the latency of a few loads.  With gate/up, 6 of 64 experts
-// of 2048 x 1408 take 17.0 us, 18.3 with the grouped product and the sum in a
-// launch each (and 3.3 more on the host); 2 of 8 of 4096 x 3584 18.0, not 19.7.  With
+// of 2048 x 1408 take 16.9 us, 18.1 with the grouped product and the sum in a
+// launch each (and 3.3 more on the host); 2 of 8 of 4096 x 3584 17.6, not 19.4.  With
 // 4 or 16 waves 0.5 us more, and with one lane in sixteen loading h no less.
 #include "kernels.h"
 #include "mx4_common.h"
@@ -101,8 +101,11 @@ __global__ __launch_bounds__(64 * KW) void mx4_one_kernel(Mx4OneArgs a) {
 
 }  // namespace
 
-// Long sums over few rows keep too few compute units busy: 2 of 2 experts of 4096 x 14336 take 54 us, 51 with two
-// launches, 8 of 32 of 2048 x 2048 25.3 and 21.7; 3 of 8 of 4096 x 4096 26.4 and 29.2.
+// Long sums over few rows keep too few compute units busy: with gate/up, 2 of 2 experts of 4096 x 14336 take 54.4 us,
+// 51.7 with the product and the sum apart, 8 of 32 of 2048 x 2048 25.2 and 21.7; 3 of 8 of 4096 x 4096 26.0 and 26.4.
+// At 300 drawn sizes (1 to 16 of 2 to 256 experts, 128 to 14336 columns, 512 to 8192 rows) the rule takes 1.011 times the
+// faster one's time in the geometric mean, 1.03 at the 90th percentile and 1.32 at worst; with 3 or 10 in the place of 5
+// it takes 1.017 and 1.013.
 bool mx4_one_supported(const Mx4OneArgs& a) { return int64_t(a.top_k) * a.C <= 5 * int64_t(a.R); }
 
 hipError_t launch_mx4_one(const Mx4OneArgs& a, hipStream_t s) {

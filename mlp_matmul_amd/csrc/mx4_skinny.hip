@@ -12,10 +12,12 @@
 // and add their partial sums in wave order through LDS, then the epilogue
 // runs on the sum: results do not depend on scheduling.
 //
-// Measured on MI355X, weights from memory: 16 rows with 4096 x 14336 11.8 us (32
+// Measured on MI355X, weights from memory: 16 rows with 4096 x 14336 12.6 us (32
 // MB of weights; they alone take 6.6 at the rate of a copy, the rest is the
-// start, two loads deep, and the sums' end), one row with 1024 x 4096 4.3, pairs
-// of 63 experts of 1408 x 2048 with four rows each 43 (4.5 TB/s).
+// start, two steps deep, the sums' end, and X: every workgroup brings all rows to
+// LDS, four loads in five), one row with 1024 x 4096 4.2, pairs of 63 experts of
+// 1408 x 2048 with one row each 43 (4.5 TB/s), with four 53 and with sixteen 65 on
+// 16-row tiles, 47 and 110 on 4-row ones.
 #include <algorithm>
 
 #include "kernels.h"
@@ -279,8 +281,8 @@ hipError_t launch_rows(const Mx4Args& a, int rows, hipStream_t s) {
 }  // namespace
 
 // Waves that split K: the fewest (2, 4 or 8; 4 with 32 input rows) that give about six waves a compute unit.  With 16
-// rows 4096 x 14336 takes 15.0 us on 4 waves and 13.2 on 8, 14336 x 4096 11.0, 13.4 and 16.4 on 2, 4 and 8, pairs of 64
-// experts of 1408 x 2048 54.6, 76.5 and 116; one row with 1024 x 4096 5.8, 4.9 and 4.3.
+// rows 4096 x 14336 takes 14.8 us on 4 waves and 12.7 on 8, 14336 x 4096 10.7, 14.1 and 18.6 on 2, 4 and 8, pairs of 64
+// experts of 1408 x 2048 with four rows each 53.5, 68 and 104; one row with 1024 x 4096 5.7, 4.8 and 4.2.
 int mx4_skinny_waves(int rows, const Mx4Args& a) {
     const int64_t bands = (int64_t(a.g.R) + 15) / 16, groups = a.g.offsets || a.g.E > 1 ? std::min<int64_t>(a.g.n, a.g.E) : 1;
     const int64_t units = bands * std::max<int64_t>(groups, a.g.offsets ? 1 : (a.g.n + rows - 1) / rows), want = 6 * int64_t(a.g.cus);

@@ -17,16 +17,21 @@
 // together, so that the workgroups of an XCD share both operands (3-10 %).
 //
 // Measured on MI355X, 8192 x 8192 weights and as many rows, us by tile:
-//   bf16 rows:   64x64 1291,  128x64 1073,  256x128 861 (1.28 PFLOP/s)
-//   4-bit rows:  64x64 533,   128x128 357,  256x256 288 (3.8 PFLOP/s)
-// Small ones for few rows: 777 rows of 14336 x 4096 in bf16 take 128, 106 and 108;
-// 32 experts with 75 rows each on 1024 x 2048 pairs 47, 40 and 62.
+//   bf16 rows:   64x64 1270,  128x64 1064,  256x128 842 (1.31 PFLOP/s)
+//   4-bit rows:  64x64 536,   128x128 356,  256x256 287 (3.8 PFLOP/s)
+// (the matrix units alone, from registers: 1.9 and 7.2 PFLOP/s).  Small ones for few
+// rows: 777 rows of 14336 x 4096 in bf16 take 125, 106 and 108; pairs of 32 experts of
+// 1024 x 2048 with 75 rows on average 47, 39 and 62, some with more than 128 (with
+// 75 each 52, 41 and 36).
 // Of the 256x256 tile's 726 thousand cycles the matrix units work 262, the LDS 213
 // on fragments and 65 on what arrives, and its loads take 143 to issue: two
 // waves a SIMD between barriers hide only part of these behind each other.  Without
-// loads it takes 428.  Four waves of 128x128 each, with twice the registers, take
-// 345 us; reading a step or more ahead into L2, loads spread among the products and
-// priorities of waves change nothing.
+// the loads of its loop it takes 237 us, not 295 (bf16 rows: 736, not 850).  Four
+// waves of 128x128 each, with twice the registers, take 345 us; reading a step or
+// more ahead into L2, loads spread among the products and priorities of waves
+// change nothing.  A tile's first loads and its epilogue overlap no other tile's work:
+// with one workgroup a compute unit they cost eight steps (mx4_matmul.hip), a third
+// of the time at 4096 columns.
 #include <type_traits>
 
 #include "kernels.h"
